@@ -559,7 +559,7 @@ def _run_own(s):
     if c["kind"] == "turnover":
         ops.kv_pages_free(s["dst"], s["table"], s["held"], s["ref"])
         ops.kv_pages_fork(s["src"], s["dst"], s["len"], s["pool"], s["table"], s["held"], s["ref"], s["ws"])
-        ops.kv_pages_reserve(s["dst"], s["grow"], c["P"], s["table"], s["held"], s["ref"])
+        ops.kv_pages_reserve(s["dst"], s["grow"], c["P"], s["table"], s["held"], s["ref"], s["ws"])
         return s["pool"], s["table"], s["held"], s["ref"]
     ops.kv_pages_compact(s["pool"], s["table"], s["held"], s["ref"], s["n_live"], s["ws"], table_out=s["table_out"],
                          refcount_out=s["ref_out"])
