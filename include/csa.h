@@ -36,7 +36,8 @@
  * shape outside the compiled set, e.g. a head dim the kernels do not handle),
  * CSA_ERR_ALIGNMENT (a pointer not 16-byte aligned), CSA_ERR_CUDA (the launch
  * failed; csa_last_cuda_error() returns the cudaError_t), CSA_ERR_TIMEOUT (a
- * bounded device wait gave up).  On any error nothing further is enqueued.
+ * bounded device wait gave up), CSA_ERR_NO_SPACE (a page pool has too few free
+ * pages; device status words only).  On any error nothing further is enqueued.
  */
 #ifndef CSA_B200_H
 #define CSA_B200_H
@@ -56,10 +57,18 @@ enum {
   CSA_ERR_UNSUPPORTED = 2,
   CSA_ERR_ALIGNMENT = 3,
   CSA_ERR_CUDA = 4,
-  CSA_ERR_TIMEOUT = 5
+  CSA_ERR_TIMEOUT = 5,
+  CSA_ERR_NO_SPACE = 6
 };
 
 enum { CSA_F32 = 0, CSA_BF16 = 1 };
+
+/* Flags of the normalising / rotating calls. */
+enum {
+  CSA_NORM = 1,         /* RMS-normalise the row before rotating it */
+  CSA_ROPE_INVERSE = 2, /* rotate by -angle */
+  CSA_ROPE_HALF = 4     /* pairs (i, i + R/2) instead of (2i, 2i + 1) */
+};
 
 /* Human-readable name of a status code (static string). */
 const char* csa_status_string(int status);
@@ -379,6 +388,154 @@ int csa_pos_advance(int32_t* pos, int B, int delta, csa_stream_t stream);
 int csa_state_gather(const void* src, int dtype, int B, int D, int src_cap,
                      const int32_t* pos, int npos, int m, int nrows,
                      void* dst, int dst_cap, csa_stream_t stream);
+
+/*
+ * qk_norm_rope -- per-head RMS norm of the queries and the shared key, and
+ * their position rotation, in one pass.  For a row x of D values of token t of
+ * sequence b, with j = q_pos0[b] + t and w the row kind's weight (NULL: ones):
+ *   y = x / sqrt(mean(x^2) + eps) * w          (flag CSA_NORM; else y = x)
+ *   pair i of the LAST R values of y is rotated by j * pos_step * inv_freq[i]
+ * (pairs (2i, 2i+1), or (i, i + R/2) with CSA_ROPE_HALF; by the negative angle
+ * with CSA_ROPE_INVERSE).  The angle is formed in 64 bits, the rest in fp32,
+ * and the result is rounded once.
+ *   q  [B, T, H, D]: batch and token strides in elements, heads contiguous;
+ *      q_out [B, T, H, D] dense
+ *   kv [B, T, D]: batch and token strides; token t goes to slot j % kv_cap of
+ *      kv_out [B, kv_cap, D] (a window ring, or kv_cap = T for a prefill);
+ *      of a call's tokens only the last kv_cap are written
+ * Either of q and kv may be NULL (its output too).  lens int32 [B] or NULL: row
+ * b has lens[b] tokens (clamped to [0, T]); outputs of tokens behind them are
+ * left as they were.  In place: q == q_out with dense strides; kv == kv_out
+ * with dense strides and kv_cap == T, when every token stays at row t.  Any
+ * other overlap of an input with an output is CSA_ERR_INVALID_ARG.
+ * Requires D in {64, 128, 256}, R % 16 == 0, 0 <= R <= D (R > 0: inv_freq
+ * float64 [R/2]), strides multiples of 8, 16-byte aligned tensors.
+ */
+int qk_norm_rope(const void* q, int64_t q_bstride, int64_t q_tstride,
+                 const void* kv, int64_t kv_bstride, int64_t kv_tstride,
+                 int dtype, int B, int T, int H, int D,
+                 const int32_t* q_pos0, const int32_t* lens, int pos_step,
+                 const double* inv_freq, int R, const float* q_weight,
+                 const float* kv_weight, float eps, int flags, void* q_out,
+                 void* kv_out, int kv_cap, csa_stream_t stream);
+
+/*
+ * Paged entries.  A pool [L, N, P, D] holds N pages of P entries for each of L
+ * layers that share the page numbering.  Row r of table int32 [R, max_pages]
+ * lists the pages of sequence r, of which held int32 [R] are in use (the others
+ * are -1): entry s of sequence r is pool[l, table[r, s / P], s % P].  refcount
+ * int32 [N] counts the rows that list a page; a page with refcount <= 0 is
+ * free.  Page ids outside [0, N) are never followed.
+ *
+ * hca_paged_append -- hca_compress ([cf-1] §3.2) of T new tokens per sequence
+ * into paged entries, from one decode token to a whole prompt.  Sequence b has
+ * seen pos0[b] tokens; tokens [pos0, pos0 + lens[b]) are a, z [B, T, D] (dense;
+ * lens NULL: T each, values clamped to [0, T]).  Every block of m tokens that
+ * completes writes its entry
+ *   e = sum_t softmax_t(z[t, c]) a[t, c]
+ * at entry index pos / m; with CSA_NORM / R > 0 the entry is normalised with
+ * `weight` and its last R values rotated by m * index * inv_freq as in
+ * qk_norm_rope.  A gate of -inf drops its token; a block whose gates are all
+ * -inf gives 0.  An entry whose page the row does not hold is dropped and
+ * recorded in the status word as CSA_ERR_NO_SPACE | 1 << 8.
+ * carry fp32 [B, 2, 3, D] holds the open block as (M, Z, A) = (max z,
+ * sum e^{z-M}, sum e^{z-M} a): part 0 its complete runs of 16 tokens, part 1 the
+ * run in progress (an empty part is (-FLT_MAX, 0, 0)).  carry_in is not read
+ * where pos0 % m == 0; carry_out may be carry_in.  Splitting a token sequence
+ * over calls in any way gives the same bits.  Sequences with pos0 < 0 or no
+ * tokens only copy their carry.
+ * pool is one layer [N, P, D] of the inputs' dtype.  Requires D in {64, 128,
+ * 256}, m >= 1, P >= 1, 16-byte aligned tensors.
+ */
+int hca_paged_append(const void* a, const void* z, int dtype, int B, int T,
+                     int D, int m, const int32_t* pos0, const int32_t* lens,
+                     const float* carry_in, float* carry_out, void* pool,
+                     int N, int P, const int32_t* table, const int32_t* held,
+                     int max_pages, const float* weight, float eps,
+                     const double* inv_freq, int R, int flags,
+                     int32_t* status, csa_stream_t stream);
+
+/*
+ * hca_prefix_attn_fwd -- HCA attention ([cf-1] §3.2, §3.3) of a batch over paged
+ * entries, for groups of sequences whose leading entries are the same pages.
+ * Same result as hca_dense_attn_fwd over each sequence's own entries (window
+ * and sink fused); what a group shares is read once for its sequences.
+ *   q, out [B, T, H, D]: query row t of sequence b is at position q_pos0[b] + t
+ *   pool [N, P, D], table [B, max_pages], held [B]: visible entries
+ *     s < (p + 1) / m whose page is not held (or out of range) are skipped
+ *   kv_raw [B, raw_cap, D]: token j at slot j % raw_cap, raw_cap >= W + T - 1
+ *   group_off [G + 1], group_seq [n_seq], group_shared [G] (device int32): group
+ *     g is the sequences group_seq[group_off[g] .. group_off[g + 1]), and their
+ *     first group_shared[g] entries lie in the pages that the group's first
+ *     member lists; n_seq = group_off[G].  Sequences that no group lists are
+ *     left as they were.
+ * A query that sees nothing (or only a sink) gives 0 and lse = -inf.
+ * Deterministic: a row's result depends on the row, its keys and
+ * max_pages * P, not on the batch, the grouping or T.
+ * bf16 with D = 128 and H <= 128 runs on tcgen05, the rest on CUDA cores
+ * (H <= 1024).  Requires D in {64, 128}, P >= 1, 16-byte aligned tensors.
+ * status: optional device status word.
+ */
+int hca_prefix_attn_fwd(const void* q, const void* pool, int N, int P,
+                        const int32_t* table, const int32_t* held,
+                        int max_pages, const int32_t* group_off,
+                        const int32_t* group_seq, const int32_t* group_shared,
+                        int G, int n_seq, const void* kv_raw,
+                        const float* sink, float tau, int W, int B, int T,
+                        int H, int D, int m, int raw_cap,
+                        const int32_t* q_pos0, void* out, float* lse,
+                        int dtype, int32_t* status, csa_stream_t stream);
+
+/*
+ * Page operations.  All lists are device int32; a call either does all of its
+ * work or, recording the reason in the status word, none of it (except
+ * kv_pages_free, which skips bad rows).  New pages are the free pages of the
+ * lowest ids, handed out in list order.  Calls that share a cache or a
+ * workspace are ordered by their stream.
+ *
+ * kv_pages_reserve: row rows[i] grows to ceil(n_entries[i] / P) pages (rows that
+ * hold enough are left alone).  Site 1: a row out of range, listed twice, or
+ * longer than max_pages; CSA_ERR_NO_SPACE: too few free pages.
+ *
+ * kv_pages_fork: the empty row dst[i] becomes a copy of the first n_entries[i]
+ * entries of row src[i]: whole pages are shared (refcount + 1), a partial last
+ * page is copied, in every layer, to a page of its own.  page_bytes is one
+ * layer's page (a multiple of 16 P); layers are N * page_bytes apart.  Site 2: a
+ * row out of range, dst not empty or listed twice, or src holding too few pages.
+ *
+ * kv_pages_free: every row in the list gives up its pages (refcount - 1) and
+ * becomes empty; a row listed twice is freed once.  Site 3: a row out of range.
+ *
+ * kv_pages_compact: the n_live pages in use move to ids [0, n_live): the k-th
+ * page in use with id >= n_live moves to the k-th free id below it.  Page data
+ * moves in place; table_out / refcount_out receive the new metadata (and may be
+ * table / refcount).  held does not change.
+ *
+ * workspace: kv_pages_workspace_size(N, n) bytes (n: list length; 0 for
+ * compact), 4-byte aligned; its contents on entry do not matter.
+ * Requires N <= 2^20; fork and compact: page_bytes / P (compact: page_bytes) a
+ * multiple of 16 bytes, pool 16-byte aligned.
+ */
+size_t kv_pages_workspace_size(int N, int n);
+int kv_pages_reserve(const int32_t* rows, const int32_t* n_entries, int n,
+                     int P, int32_t* table, int32_t* held, int R,
+                     int max_pages, int32_t* refcount, int N, void* workspace,
+                     size_t ws_bytes, int32_t* status, csa_stream_t stream);
+int kv_pages_fork(const int32_t* src, const int32_t* dst,
+                  const int32_t* n_entries, int n, int P, int32_t* table,
+                  int32_t* held, int R, int max_pages, int32_t* refcount,
+                  int N, void* pool, int L, int64_t page_bytes,
+                  void* workspace, size_t ws_bytes, int32_t* status,
+                  csa_stream_t stream);
+int kv_pages_free(const int32_t* rows, int n, int32_t* table, int32_t* held,
+                  int R, int max_pages, int32_t* refcount, int N,
+                  int32_t* status, csa_stream_t stream);
+int kv_pages_compact(const int32_t* table, const int32_t* held, int R,
+                     int max_pages, const int32_t* refcount, int N,
+                     void* pool, int L, int64_t page_bytes,
+                     int32_t* table_out, int32_t* refcount_out,
+                     int32_t* n_live, void* workspace, size_t ws_bytes,
+                     csa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -417,6 +417,7 @@ const char* csa_status_string(int status) {
     case CSA_ERR_ALIGNMENT: return "CSA_ERR_ALIGNMENT";
     case CSA_ERR_CUDA: return "CSA_ERR_CUDA";
     case CSA_ERR_TIMEOUT: return "CSA_ERR_TIMEOUT";
+    case CSA_ERR_NO_SPACE: return "CSA_ERR_NO_SPACE";
     default: return "CSA_ERR_UNKNOWN";
   }
 }

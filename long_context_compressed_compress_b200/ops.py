@@ -17,7 +17,8 @@ LIB_PATH = os.path.join(_HERE, "libcsa_b200.so")
 
 CSA_F32, CSA_BF16 = 0, 1
 STATUS = {0: "CSA_OK", 1: "CSA_ERR_INVALID_ARG", 2: "CSA_ERR_UNSUPPORTED", 3: "CSA_ERR_ALIGNMENT",
-          4: "CSA_ERR_CUDA", 5: "CSA_ERR_TIMEOUT"}
+          4: "CSA_ERR_CUDA", 5: "CSA_ERR_TIMEOUT", 6: "CSA_ERR_NO_SPACE"}
+NORM, ROPE_INVERSE, ROPE_HALF = 1, 2, 4
 
 
 class CsaError(RuntimeError):
@@ -60,6 +61,14 @@ _SIGS = {
     "csa_pos_advance": ([P, I, I, P], I),
     "csa_decode_update": ([P] * 8 + [I] * 8 + [P] * 12 + [F, P, P], I),
     "csa_state_gather": ([P, I, I, I, I, P, I, I, I, P, I, P], I),
+    "qk_norm_rope": ([P, I64, I64, P, I64, I64, I, I, I, I, I, P, P, I, P, I, P, P, F, I, P, P, I, P], I),
+    "hca_paged_append": ([P, P, I, I, I, I, I, P, P, P, P, P, I, I, P, P, I, P, F, P, I, I, P, P], I),
+    "hca_prefix_attn_fwd": ([P, P, I, I, P, P, I, P, P, P, I, I, P, P, F, I, I, I, I, I, I, I, P, P, P, I, P, P], I),
+    "kv_pages_workspace_size": ([I, I], SZ),
+    "kv_pages_reserve": ([P, P, I, I, P, P, I, I, P, I, P, SZ, P, P], I),
+    "kv_pages_fork": ([P, P, P, I, I, P, P, I, I, P, I, P, I, I64, P, SZ, P, P], I),
+    "kv_pages_free": ([P, I, P, P, I, I, P, I, P, P], I),
+    "kv_pages_compact": ([P, P, I, I, P, I, P, I, I64, P, P, P, P, SZ, P], I),
     "grouped_out_proj": ([P, I, I, I, I, I, P, P, I, P, P, P, P], I),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -269,3 +278,193 @@ def grouped_out_proj(o, w1, w2, y, out, status=None, stream=None):
     _check("grouped_out_proj", lib.grouped_out_proj(
         _ptr(o), M, H, D, g, d_g, _ptr(w1), _ptr(w2), w2.shape[0], _ptr(y), _ptr(out), _ptr(status),
         _stream(stream)))
+
+
+def _rows_of(x, heads):
+    """(pointer, batch stride, token stride) of x [B, T, (H,) D] whose heads and
+    values are dense; the batch and token strides are free."""
+    if x is None:
+        return None, 0, 0
+    if not x.is_cuda:
+        raise ValueError("tensor must be on the GPU")
+    B, T = x.shape[:2]
+    inner = x[0, 0] if B and T else x.new_empty(x.shape[2:])
+    if not inner.is_contiguous():
+        raise ValueError("the values of a token must be contiguous")
+    row = x.shape[-1] * (x.shape[2] if heads else 1)
+    ts = x.stride(1) if T > 1 else row
+    return x.data_ptr(), (x.stride(0) if B > 1 else T * ts), ts
+
+
+def _typed(t, dtype, name, shape=None):
+    """The pointer of an optional contiguous tensor of one dtype (and shape)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _same(*ts):
+    """All (non-None) tensors on one device, the current one."""
+    dev = {t.device for t in ts if t is not None}
+    if len(dev) > 1:
+        raise ValueError(f"tensors are on several devices: {sorted(map(str, dev))}")
+    for d in dev:
+        if d.type == "cuda" and d.index != torch.cuda.current_device():
+            raise ValueError(f"tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rope_flags(norm, interleaved, inverse):
+    return (NORM if norm else 0) | (0 if interleaved else ROPE_HALF) | (ROPE_INVERSE if inverse else 0)
+
+
+def qk_norm_rope(q, kv, q_out, kv_out, q_pos0, inv_freq=None, q_weight=None, kv_weight=None, eps=1e-6, norm=True,
+                 interleaved=True, inverse=False, pos_step=1, lens=None, stream=None):
+    """RMS norm per head and position rotation of the queries q [B, T, H, D] and
+    the shared key kv [B, T, D] in one pass (either pair may be None).  Token t
+    is at j = q_pos0[b] + t and is rotated by j * pos_step * inv_freq; its key
+    goes to slot j % cap of kv_out [B, cap, D].  q and kv may be views with free
+    batch and token strides (slices of one projection's output)."""
+    _same(q, kv, q_out, kv_out, q_pos0, inv_freq, q_weight, kv_weight, lens)
+    if (q is None) != (q_out is None) or (kv is None) != (kv_out is None) or (q is None and kv is None):
+        raise ValueError("q with q_out, kv with kv_out, at least one pair")
+    x = q if q is not None else kv
+    B, T, D = x.shape[0], x.shape[1], x.shape[-1]
+    H = q.shape[2] if q is not None else 0
+    cap = 0
+    if q is not None and (q_out.dtype != q.dtype or q_out.shape != q.shape):
+        raise ValueError("q_out must have q's shape and dtype")
+    if kv is not None:
+        cap = kv_out.shape[1]
+        if kv.dtype != x.dtype or kv_out.dtype != x.dtype or kv.shape != (B, T, D) or kv_out.shape != (B, cap, D):
+            raise ValueError("kv must be [B, T, D] and kv_out [B, cap, D], of q's dtype")
+    if T == 0 or B == 0:
+        return
+    qp, qb, qt = _rows_of(q, True)
+    kp, kb, kt = _rows_of(kv, False)
+    R = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _check("qk_norm_rope", lib.qk_norm_rope(
+        qp, qb, qt, kp, kb, kt, _dt(x), B, T, H, D, _typed(q_pos0, torch.int32, "q_pos0", (B,)),
+        _typed(lens, torch.int32, "lens", (B,)), pos_step, _typed(inv_freq, torch.float64, "inv_freq"), R,
+        _typed(q_weight, torch.float32, "q_weight", (D,)), _typed(kv_weight, torch.float32, "kv_weight", (D,)), eps,
+        _rope_flags(norm, interleaved, inverse), _ptr(q_out), _ptr(kv_out), cap, _stream(stream)))
+
+
+def _cache_args(table, held, refcount=None):
+    R, maxp = table.shape
+    return (_typed(table, torch.int32, "table"), _typed(held, torch.int32, "held", (R,)), R, maxp,
+            _typed(refcount, torch.int32, "refcount"))
+
+
+def hca_paged_append(a, z, pos0, carry, pool, table, held, m, carry_out=None, lens=None, norm=False, weight=None,
+                     eps=1e-6, inv_freq=None, interleaved=True, inverse=False, status=None, stream=None):
+    """Pool new tokens a, z [B, T, D] (gates z) into paged entries pool [N, P, D];
+    carry [B, 2, 3, D] float32 holds the open blocks and is updated in place, or
+    into carry_out.  Entries are optionally normalised and rotated at m * index."""
+    carry_out = carry if carry_out is None else carry_out
+    _same(a, z, pos0, carry, carry_out, pool, table, held, lens, weight, inv_freq, status)
+    B, T, D = a.shape
+    if z.shape != a.shape or z.dtype != a.dtype or pool.dtype != a.dtype or pool.dim() != 3 or pool.shape[2] != D:
+        raise ValueError("a and z must be [B, T, D], pool [N, P, D], of one dtype")
+    if table.shape[0] != B:
+        raise ValueError("table must have one row per sequence")
+    tp, hp, _, maxp, _ = _cache_args(table, held)
+    _check("hca_paged_append", lib.hca_paged_append(
+        _ptr(a), _ptr(z), _dt(a), B, T, D, m, _typed(pos0, torch.int32, "pos0", (B,)),
+        _typed(lens, torch.int32, "lens", (B,)), _typed(carry, torch.float32, "carry", (B, 2, 3, D)),
+        _typed(carry_out, torch.float32, "carry_out", (B, 2, 3, D)), _ptr(pool), pool.shape[0], pool.shape[1], tp, hp,
+        maxp, _typed(weight, torch.float32, "weight", (D,)), eps, _typed(inv_freq, torch.float64, "inv_freq"),
+        0 if inv_freq is None else 2 * inv_freq.numel(), _rope_flags(norm, interleaved, inverse),
+        _typed(status, torch.int32, "status"), _stream(stream)))
+
+
+def hca_prefix_attn_fwd(q, pool, table, held, groups, kv_raw, sink, tau, W, q_pos0, out, m, lse=None, raw_cap=None,
+                        status=None, stream=None):
+    """HCA attention of q [B, T, H, D] over paged entries pool [N, P, D], the raw
+    window kv_raw [B, raw_cap, D] and the sink; ``groups`` (paged.PrefixGroups)
+    names the sequences that share their first pages."""
+    B, T, H, D = q.shape
+    _same(q, pool, table, held, groups.off, kv_raw, sink, q_pos0, out, lse, status)
+    if pool.dtype != q.dtype or pool.dim() != 3 or pool.shape[2] != D or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("pool must be [N, P, D] and out [B, T, H, D], of q's dtype")
+    if table.shape[0] != B or groups.B != B:
+        raise ValueError("table and groups must be those of the batch")
+    if W and (kv_raw is None or kv_raw.dtype != q.dtype or kv_raw.dim() != 3 or kv_raw.shape[0] != B
+              or kv_raw.shape[2] != D or (raw_cap is not None and raw_cap > kv_raw.shape[1])):
+        raise ValueError("kv_raw must be [B, raw_cap, D] of q's dtype")
+    raw_cap = (kv_raw.shape[1] if kv_raw is not None else 1) if raw_cap is None else raw_cap
+    if W and raw_cap != kv_raw.shape[1] and B > 1:
+        raise ValueError("raw_cap must be kv_raw's")
+    tp, hp, _, maxp, _ = _cache_args(table, held)
+    _check("hca_prefix_attn_fwd", lib.hca_prefix_attn_fwd(
+        _ptr(q), _ptr(pool), pool.shape[0], pool.shape[1], tp, hp, maxp, _ptr(groups.off), _ptr(groups.seq),
+        _ptr(groups.shared), groups.G, groups.n_seq, _ptr(kv_raw), _typed(sink, torch.float32, "sink", (H,)), tau, W,
+        B, T, H, D, m, raw_cap, _typed(q_pos0, torch.int32, "q_pos0", (B,)), _ptr(out),
+        _typed(lse, torch.float32, "lse", (B, T, H)), _dt(q), _typed(status, torch.int32, "status"),
+        _stream(stream)))
+
+
+def kv_pages_workspace_size(N, n):
+    return int(lib.kv_pages_workspace_size(N, n))
+
+
+def _ws(workspace):
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def _layers(pool, refcount):
+    """(pointer, L, bytes of one layer's page) of pool [L, N, P, D]."""
+    if pool.dim() != 4 or pool.shape[1] != refcount.numel():
+        raise ValueError("pool must be [L, N, P, D] with refcount [N]")
+    return _ptr(pool), pool.shape[0], pool.shape[2] * pool.shape[3] * pool.element_size()
+
+
+def kv_pages_reserve(rows, n_entries, P, table, held, refcount, workspace, status=None, stream=None):
+    """Grow the listed rows to hold n_entries entries each (pages of P)."""
+    _same(rows, n_entries, table, held, refcount, workspace, status)
+    tp, hp, R, maxp, rp = _cache_args(table, held, refcount)
+    n = rows.numel()
+    _check("kv_pages_reserve", lib.kv_pages_reserve(
+        _typed(rows, torch.int32, "rows", (n,)), _typed(n_entries, torch.int32, "n_entries", (n,)), n, P, tp, hp, R,
+        maxp, rp, refcount.numel(), *_ws(workspace), _typed(status, torch.int32, "status"), _stream(stream)))
+
+
+def kv_pages_fork(src, dst, n_entries, pool, table, held, refcount, workspace, status=None, stream=None):
+    """Make each empty row dst[i] share the first n_entries[i] entries of src[i];
+    pool [L, N, P, D] (a partial last page is copied in every layer)."""
+    _same(src, dst, n_entries, pool, table, held, refcount, workspace, status)
+    tp, hp, R, maxp, rp = _cache_args(table, held, refcount)
+    n = dst.numel()
+    pp, L, page = _layers(pool, refcount)
+    _check("kv_pages_fork", lib.kv_pages_fork(
+        _typed(src, torch.int32, "src", (n,)), _typed(dst, torch.int32, "dst", (n,)),
+        _typed(n_entries, torch.int32, "n_entries", (n,)), n, pool.shape[2], tp, hp, R, maxp, rp, refcount.numel(), pp,
+        L, page, *_ws(workspace), _typed(status, torch.int32, "status"), _stream(stream)))
+
+
+def kv_pages_free(rows, table, held, refcount, status=None, stream=None):
+    """Give up the pages of the listed rows."""
+    _same(rows, table, held, refcount, status)
+    tp, hp, R, maxp, rp = _cache_args(table, held, refcount)
+    n = rows.numel()
+    _check("kv_pages_free", lib.kv_pages_free(
+        _typed(rows, torch.int32, "rows", (n,)), n, tp, hp, R, maxp, rp, refcount.numel(),
+        _typed(status, torch.int32, "status"), _stream(stream)))
+
+
+def kv_pages_compact(pool, table, held, refcount, n_live, workspace, table_out=None, refcount_out=None, stream=None):
+    """Move the pages in use to the ids [0, n_live) (pool [L, N, P, D] in place);
+    the new metadata goes to table_out / refcount_out (default: in place) and
+    the number of pages in use to n_live int32 [1]."""
+    table_out = table if table_out is None else table_out
+    refcount_out = refcount if refcount_out is None else refcount_out
+    _same(pool, table, held, refcount, n_live, workspace, table_out, refcount_out)
+    tp, hp, R, maxp, rp = _cache_args(table, held, refcount)
+    pp, L, page = _layers(pool, refcount)
+    _check("kv_pages_compact", lib.kv_pages_compact(
+        tp, hp, R, maxp, rp, refcount.numel(), pp, L, page, _typed(table_out, torch.int32, "table_out", table.shape),
+        _typed(refcount_out, torch.int32, "refcount_out", refcount.shape),
+        _typed(n_live, torch.int32, "n_live", (1,)), *_ws(workspace), _stream(stream)))
