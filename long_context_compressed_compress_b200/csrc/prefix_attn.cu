@@ -27,5 +27,6 @@ extern "C" int hca_prefix_attn_fwd(const void* q, const void* pool, int N, int P
   CSA_REQUIRE(a.status != nullptr, CSA_ERR_CUDA);
   a.tau = tau; a.N = N; a.P = P; a.max_pages = max_pages; a.G = G; a.n_seq = n_seq; a.W = W; a.B = B; a.T = T;
   a.H = H; a.m = m; a.raw_cap = raw_cap;
+  if (dtype == CSA_BF16 && D == 128 && H <= 128) return launch_prefix_attn_tc(a, reinterpret_cast<cudaStream_t>(stream));
   return launch_prefix_attn_simt(a, D, dtype, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -32,5 +32,6 @@ __device__ __forceinline__ int visible_entries(const PrefixAttnArgs& a, int b, l
 }
 
 int launch_prefix_attn_simt(const PrefixAttnArgs& a, int D, int dtype, cudaStream_t st);
+int launch_prefix_attn_tc(const PrefixAttnArgs& a, cudaStream_t st);   // bf16, D = 128, H <= 128
 
 }  // namespace csa
