@@ -10,7 +10,7 @@
 //                                      read with its dims as N)
 // Key tiles come in three kinds:
 //   shared  128 entries that every row of the job sees, loaded once for all;
-//   own     128 entries of one pair's sequence;
+//   own     128 entries of one sequence (its pairs that see equally many share a tile);
 //   window  8 runs of 16 raw tokens, each of one pair.
 // Own and window tiles concern some rows only.  The PV MMA of such a tile writes
 // those rows' lanes alone (its lane mask), so a row's sum holds its own keys
@@ -25,18 +25,23 @@
 // and a row's rescaling depends on the row: its bits do not depend on batch or
 // grouping.
 //
-// Softmax.  Exact online form with a lazy stabiliser: a row's M starts as its
-// first maximum and moves (rescaling O in tensor memory) only when a later one
-// exceeds it by more than 2^8, so weights stay below 2^8 and sums in fp32.
+// Softmax.  A row's stabiliser M is the maximum of its first tile in the rank, and
+// stays: weights 2^(l - M) and their sums keep fp32's (and, in P, bf16's) relative
+// precision at any scale, so M only has to keep them in range.  A row in which
+// a later weight passes 2^100 is flagged and computed again, exactly, on CUDA
+// cores with a running maximum; a weight below 2^-126 of the first tile's
+// largest is lost against it anyway.  So once M is there a tile needs no maximum and no
+// word from the tiles before (a running one took a third of a tile's time).
 // P is rounded to bf16 for the MMA (a half step of 2^-9 a weight, of the size
-// of the output's own rounding); the row sum adds the unrounded weights.
+// of the output's own rounding); the row sum adds the unrounded weights, by tile
+// parity (i / c) % 2.
 //
 // Roles (12 warps).  Softmax warpgroups 0 and 1 (warps 0 - 3, 4 - 7) take the even
-// and the odd tiles, with S and P buffers of their own and one O; they hand each
-// row's M from tile to tile.  Producer warps 8, 9 (64 tile rows each): whole
-// tiles by TMA boxes of a page (or its largest power of two of rows), the others
-// by 16-byte asynchronous copies.  Warp 10 issues QK (a warpgroup's next as soon
-// as it has read the last S), warp 11 PV.
+// and the odd tiles, a thread a row; S and P are double buffered, O is one.  Warp
+// 8 loads entries: by TMA boxes of a page (or the largest power of two of its rows),
+// row by row where a page is missing; warp 9 window rows, by 16-byte asynchronous
+// copies.  Warp 10 issues QK (a warpgroup's next as soon as it has read the last
+// S), warp 11 PV.
 //
 // All waits are bounded in time and every thread reaches the cluster barriers.
 #include <cuda.h>
@@ -55,11 +60,11 @@ constexpr int kTileBytes = kTile * kDim * 2;
 constexpr int kRegion = kTile * 128;          // the 64-dim half of a tile
 constexpr int kMaxCluster = 8;
 constexpr int kPairs = 16;                    // most pairs of a job
-constexpr int kProdWarps = 2, kProd0 = 8, kQkWarp = 10, kPvWarp = 11;
+constexpr int kSoftWarps = 8, kEntryWarp = 8, kWindowWarp = 9, kQkWarp = 10, kPvWarp = 11;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColP = 256, kColO = 384;   // S, P of warpgroup w at 128 w, 256 + 64 w
-constexpr float kLazy = 8.f;                  // log2 of the growth a stabiliser lets pass
+constexpr uint32_t kColS = 0, kColP = 256, kColO = 384;   // S, P of tile parity w at 128 w, 256 + 64 w
+constexpr float kMost = 1.2676506e30f;        // 2^100: a row's weights beyond it are done again
 
 enum : int { kShared = 0, kOwn = 1, kWindow = 2, kEnd = 3 };
 
@@ -67,25 +72,37 @@ struct Pair {
   int b, t, n, nw;        // sequence, token; visible entries; window rows (0 .. W)
   int p;                  // position
 };
-struct Desc {
-  int kind, u, nk, seg0;  // nk: 16-key steps of the PV
+// A tile: its kind; own: the pairs u .. u + m - 1; cnt: keys that are there (shared,
+// own) or runs (window); seg0: the window's first run, an own tile's parity.  One
+// 16-byte word.
+struct __align__(16) Desc {
+  int kind, um, cnt, seg0;
+  __device__ int u() const { return um & 0xff; }
+  __device__ int m() const { return um >> 8; }
 };
+__device__ __forceinline__ Desc make_desc(int kind, int u, int m, int cnt, int seg0) {
+  return Desc{kind, u | (m << 8), cnt, seg0};
+}
 
 struct __align__(1024) Smem {
   uint8_t q[kTileBytes];
-  uint8_t kv[kStages][kTileBytes];     // the first half is reused for the CTA's O (64 KB) at the end
-  uint64_t kv_full[kStages], kv_empty[kStages], q_full, s_full[2], s_free[2], p_full[2], pv_done[2];
-  uint64_t drain[2];
-  unsigned long long m_next[2][kTile], l_next[2][kTile];   // (tile, value) on its way between the warpgroups
+  uint8_t kv[kStages][kTileBytes];     // reused at the end: the CTA's O (64 KB), then the ranks' parts of its rows (64 KB)
+  uint64_t kv_full[kStages], kv_empty[kStages], win_go[kStages], q_full, s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t drain[2], joined;
+  // (tile, value) on its way between the warpgroups: a row's M (by the tile parity it
+  // comes from) and sums (by the parity they belong to)
+  unsigned long long m_next[2][kTile], l_sum[2][kTile];
+  uint8_t redo[kTile];
   float m[kTile], l[kTile];            // the CTA's, at the end
-  uint32_t valid[kStages][4];
+  uint4 valid[kStages];                // which rows are keys
+  int rows[32];                        // page chunks on their way to the boxes
   Desc desc[kStages];
-  int s_stage[2];
   float sink_l2[kTile];                // by head
   Pair pair[kPairs];
   int npair;
   int group, tile, shared, leader;
   uint32_t tmem;
+  int tiles;                           // of this CTA, once the last S is on its way
   int abort_flag;
 };
 
@@ -93,6 +110,8 @@ struct Args : PrefixAttnArgs {
   float scale_log2;     // |tau| log2(e)
   int negate;           // tau < 0: Q is negated on load
   int box;              // rows of a page chunk that a TMA box brings (0: pages too odd)
+  uint32_t p_mul, p_shift;   // key / P = (key p_mul) >> (32 + p_shift), P > 1
+  int log_c;
   uint32_t h_inv;       // ceil(2^16 / H): r / H = r h_inv >> 16 for r < 128
   int c;                // cluster size
   int ppt;              // pairs a job
@@ -124,6 +143,11 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, const Arg
   atomicCAS(a.status, 0, CSA_ERR_TIMEOUT | (site << 8));
   *abort_flag = 1;
   return false;
+}
+// Bounded wait of one thread.
+__device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity, const Args& a, volatile int* abort_flag,
+                                      int site) {
+  return try_wait(bar, parity, a.hint_ns) || wait_slow(bar, parity, a, abort_flag, site);
 }
 // Bounded wait with the same answer in every lane of the warp.
 __device__ __forceinline__ bool waitw(uint64_t* bar, uint32_t parity, const Args& a, volatile int* abort_flag,
@@ -180,21 +204,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// (a0, a1) * b + c on the packed fp32 pipe
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b), "f"(c));
-}
-__device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %3};\n\t"
-      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "+f"(x0), "+f"(x1)
-      : "f"(y0), "f"(y1));
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -210,17 +219,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
                  "=r"((r)[22]), "=r"((r)[23]), "=r"((r)[24]), "=r"((r)[25]), "=r"((r)[26]),               \
                  "=r"((r)[27]), "=r"((r)[28]), "=r"((r)[29]), "=r"((r)[30]), "=r"((r)[31])                \
                : "r"(taddr))
-
-#define PA_TMEM_LD_X8(taddr, r)                                                                           \
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"                   \
-               : "=r"((r)[0]), "=r"((r)[1]), "=r"((r)[2]), "=r"((r)[3]), "=r"((r)[4]), "=r"((r)[5]),      \
-                 "=r"((r)[6]), "=r"((r)[7])                                                               \
-               : "r"(taddr))
-#define PA_TMEM_ST_X8(taddr, r)                                                                           \
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),      \
-               "r"((r)[0]), "r"((r)[1]), "r"((r)[2]), "r"((r)[3]), "r"((r)[4]), "r"((r)[5]), "r"((r)[6]), \
-               "r"((r)[7])                                                                                \
-               : "memory")
 
 // D[tmem] += A[tmem] * B[smem]; lanes whose bit is set in `off` are not written.
 __device__ __forceinline__ void mma_ts_lanes(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -239,6 +237,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc)
       : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(n)
+               : "memory");
 }
 // K-major operand, 16-element step j; the same tile with its rows as K.
 __device__ __forceinline__ uint64_t desc_kmajor(uint32_t base, int j) {
@@ -284,13 +289,16 @@ __device__ __forceinline__ float ld_peer(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+__device__ __forceinline__ uint32_t ld_peer_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+// Copy shared memory to a peer's; its mbarrier counts the bytes.
+__device__ __forceinline__ void push_to_peer(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+               : "memory");
 }
 
 // ----------------------------------------------------------------- set-up
@@ -368,6 +376,67 @@ __device__ void load_pairs(const Args& a, Smem& sm, int o0, int members) {
   }
 }
 
+// One row again on CUDA cores (a warp; a lane 4 dims): the online softmax in fp32 over
+// the row's entries and window, as the definition states.
+__device__ __noinline__ void row_exact(const Args& a, const Pair& pr, int h, float sink_l2) {
+  const int lane = threadIdx.x & 31;
+  const size_t row = (static_cast<size_t>(pr.b) * a.T + pr.t) * a.H + h;
+  const float sl2 = a.negate ? -a.scale_log2 : a.scale_log2;
+  float q[4], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+  auto load4 = [&](const __nv_bfloat16* p, float x[4]) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * lane);
+    x[0] = __uint_as_float(v.x << 16);
+    x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16);
+    x[3] = __uint_as_float(v.y & 0xffff0000u);
+  };
+  load4(static_cast<const __nv_bfloat16*>(a.q) + row * kDim, q);
+  auto visit = [&](const __nv_bfloat16* key) {
+    float k[4];
+    load4(key, k);
+    float x = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    x *= sl2;
+    const float mn = x > m ? x : m;
+    const float f = mn > -INFINITY ? exp2f(m - mn) : 1.f, w = exp2f(x - (mn > -INFINITY ? mn : 0.f));
+    l = fmaf(l, f, w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = fmaf(acc[e], f, w * k[e]);
+    m = mn;
+  };
+  const int32_t* tab = a.table + static_cast<size_t>(pr.b) * a.max_pages;
+  for (int s = 0; s < pr.n; ++s) {
+    const int id = tab[s / a.P];
+    if (id >= 0 && id < a.N)
+      visit(static_cast<const __nv_bfloat16*>(a.pool) + (static_cast<size_t>(id) * a.P + s % a.P) * kDim);
+  }
+  for (int j = 0; j < pr.nw; ++j)
+    visit(static_cast<const __nv_bfloat16*>(a.kv_raw) +
+          (static_cast<size_t>(pr.b) * a.raw_cap + (pr.p - j) % a.raw_cap) * kDim);
+  float sc = 0.f, lse = -INFINITY;
+  if (l != 0.f) {
+    const float X = fmaxf(m, sink_l2), f = exp2f(m - X);
+    sc = __fdiv_rn(f, fmaf(l, f, exp2f(sink_l2 - X)));
+    lse = (m + log2f(l)) * 0.6931471805599453f;
+  }
+  uint2 o2;
+  o2.x = pack_bf16(acc[0] * sc, acc[1] * sc);
+  o2.y = pack_bf16(acc[2] * sc, acc[3] * sc);
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kDim + lane * 4) = o2;
+  if (a.lse && lane == 0) a.lse[row] = lse;
+}
+
+// How many of this rank's entry tiles lie in [i0, ceil(n / 128)).
+__device__ __forceinline__ int tiles_of(int i0, int n, int log_c) {
+  const int end = static_cast<int>((static_cast<uint32_t>(n) + kTile - 1) / kTile);
+  return end > i0 ? (end - i0 + (1 << log_c) - 1) >> log_c : 0;
+}
+// Pair u continues the tiles of pair u - 1: the same sequence, as many entries.
+__device__ __forceinline__ bool joined(const Smem& sm, int u) {
+  return u > 0 && sm.pair[u].b == sm.pair[u - 1].b && sm.pair[u].n == sm.pair[u - 1].n;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_constant__ Args a,
                                                                   const __grid_constant__ CUtensorMap pool_map) {
   extern __shared__ __align__(1024) uint8_t pa_smem_raw[];
@@ -385,10 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     else if (lane == 0) sm.group = -1;
   } else if (warp == 1 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.kv_full[s], 32 * kProdWarps + kProdWarps);
+      mbar_init(&sm.kv_full[s], 33);
       mbar_init(&sm.kv_empty[s], 1);
+      mbar_init(&sm.win_go[s], 1);
     }
-    mbar_init(&sm.q_full, 256);
+    mbar_init(&sm.q_full, 32 * kSoftWarps);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&sm.s_full[w], 2);
       mbar_init(&sm.s_free[w], 128);
@@ -396,9 +466,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       mbar_init(&sm.pv_done[w], 1);
       mbar_init(&sm.drain[w], 1);
     }
+    mbar_init(&sm.joined, 1);
     sm.abort_flag = 0;
+    sm.tiles = INT32_MAX;
     fence_mbar_init();
-  } else if (warp < 6) {
+  } else if (warp >= 2 && warp < 6) {
     const int h = threadIdx.x - 64;
     sm.sink_l2[h] = a.sink && h < a.H ? a.sink[h] * 1.4426950408889634f : -INFINITY;
   } else if (warp == kQkWarp) {
@@ -410,102 +482,144 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   const bool idle = sm.group < 0;      // the same in every CTA of the cluster
+  const int segs = max(a.win_run / 16, 1);
+  // the first entry tile of this rank behind the shared ones
+  const int own0 = idle ? 0 : sm.shared + ((rank - sm.shared) & (a.c - 1));
 
-  if (!idle && warp >= kProd0 && warp < kProd0 + kProdWarps) {
+  if (!idle && (warp == kEntryWarp || warp == kWindowWarp)) {
     // ================================================================= producers
-    const int pw = warp - kProd0, half = lane >> 4, c = lane & 15;
-    const __nv_bfloat16* pool = static_cast<const __nv_bfloat16*>(a.pool) + c * 8;
-    const __nv_bfloat16* ring = static_cast<const __nv_bfloat16*>(a.kv_raw) + c * 8;
-    int g = 0;
+    const int half = lane >> 4, c = lane & 15;
     bool ok = true;
-    int armed[kStages];                // last use of each stage by TMA
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) armed[s] = -1;
-    // Entry `key` of sequence b as a row of the pool, or -1.
-    auto entry = [&](int b, int key, int n) {
-      if (key >= n) return -1;
-      const int id = a.table[static_cast<size_t>(b) * a.max_pages + key / a.P];
-      return id >= 0 && id < a.N ? id * a.P + key % a.P : -1;
-    };
-    auto announce = [&](int stage, const Desc& d, uint32_t v0, uint32_t v1) {
-      sm.valid[stage][2 * pw] = v0;
-      sm.valid[stage][2 * pw + 1] = v1;
-      if (pw == 0) sm.desc[stage] = d;
-    };
-    // One tile, row by row: src(r) gives the row of the pool (or ring) for tile row r, or -1.
-    auto put = [&](const Desc& d, auto&& src) {
+    // The entry tiles come first, then the window's, then the end.  The entry warp sees
+    // every stage through its uses (an mbarrier tells a phase from the next alone,
+    // so a waiter must not skip one) and opens the window warp's stages to it.
+    int mine = 0;
+    if (lane < sm.npair && !joined(sm, lane)) mine = tiles_of(own0, sm.pair[lane].n, a.log_c);
+    const int entry_tiles = tiles_of(rank, sm.shared * kTile, a.log_c) + __reduce_add_sync(0xffffffffu, mine);
+    const int win_tiles = rank * a.win_run < a.W ? (sm.npair * segs + 7) / 8 : 0;
+    int g = warp == kEntryWarp ? 0 : entry_tiles;
+    auto stage_free = [&]() {
       const int stage = g % kStages, use = g / kStages;
-      const bool data = d.kind != kEnd;
-      const int r0 = 64 * pw + lane;
-      const int x0 = data ? src(r0) : -1, x1 = data ? src(r0 + 32) : -1;
-      const uint32_t v0 = __ballot_sync(0xffffffffu, x0 >= 0), v1 = __ballot_sync(0xffffffffu, x1 >= 0);
-      if (use >= 1 && !waitw(&sm.kv_empty[stage], (use - 1) & 1, a, abort_flag, 20)) return false;
-      if (data) {
-        const __nv_bfloat16* base = d.kind == kWindow ? ring : pool;
-        const uint32_t dbase = smem_u32(sm.kv[stage]) + (c >> 3) * kRegion + (64 * pw + half) * 128;
-        const uint32_t cx = static_cast<uint32_t>((c & 7) ^ half);
+      if (use < 1) return true;
+      if (warp == kEntryWarp) return waitw(&sm.kv_empty[stage], (use - 1) & 1, a, abort_flag, 20);
+      // the stage's first use by a window slot that waits
+      const int first = max(1, (entry_tiles - stage + kStages - 1) / kStages);
+      return waitw(&sm.win_go[stage], (use - first) & 1, a, abort_flag, 32);
+    };
+    // One tile row by row: src(r) gives the row of `from` for tile row r, or -1.
+    auto put = [&](const Desc& d, const void* from, int rows, auto&& src) {
+      const int stage = g % kStages;
+      int x[4];
+      uint32_t bits[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = 32 * i < rows ? src(32 * i + lane) : -1;
+        bits[i] = __ballot_sync(0xffffffffu, x[i] >= 0);
+      }
+      if (!stage_free()) { ok = false; return; }
+      const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(from) + c * 8;
+      const uint32_t dbase = smem_u32(sm.kv[stage]) + (c >> 3) * kRegion + half * 128;
+      const uint32_t cx = static_cast<uint32_t>((c & 7) ^ half);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (32 * i >= rows) break;
 #pragma unroll 8
-        for (int j = 0; j < 32; ++j) {
-          const int x = __shfl_sync(0xffffffffu, j < 16 ? x0 : x1, (2 * j + half) & 31);
-          const uint32_t dst = dbase + j * 256 + ((cx ^ static_cast<uint32_t>((2 * j) & 7)) << 4);
-          cp_async16(dst, base + static_cast<size_t>(max(x, 0)) * kDim, x >= 0 ? 16u : 0u);
+        for (int j = 0; j < 16; ++j) {
+          const int y = __shfl_sync(0xffffffffu, x[i], 2 * j + half);
+          const uint32_t dst = dbase + (16 * i + j) * 256 + ((cx ^ static_cast<uint32_t>((2 * j) & 7)) << 4);
+          cp_async16(dst, base + static_cast<size_t>(max(y, 0)) * kDim, y >= 0 ? 16u : 0u);
         }
       }
       cp_async_mbar_arrive(&sm.kv_full[stage]);
       if (lane == 0) {
-        announce(stage, d, v0, v1);
+        sm.valid[stage] = make_uint4(bits[0], bits[1], bits[2], bits[3]);
+        sm.desc[stage] = d;
         mbar_arrive(&sm.kv_full[stage]);
       }
       ++g;
-      return true;
     };
-    // This rank's entry tiles i, i + c, .. of sequence b below n: by TMA where all
-    // 128 entries are there, else row by row.  The page chunks of the next 32 /
-    // boxes tiles are looked up at once, a lane each (one tile at a time, the
-    // lookup's latency alone would pace the loop at 2000 cycles a tile).
-    const int boxes = a.box ? 64 / a.box : 32;         // of this warp's 64 rows
-    const int ahead = 32 / boxes;
-    auto put_tiles = [&](int kind, int u, int b, int i, int n) {
-      int rows = -1;
-      for (int k = 0; ok && static_cast<long long>(i) * kTile < n; i += a.c, k = k + 1 == ahead ? 0 : k + 1) {
-        const int key0 = i * kTile;
-        const Desc d{kind, u, (min(kTile, n - key0) + 15) / 16, 0};
-        if (a.box && k == 0) {
-          const long long key = (i + static_cast<long long>(lane / boxes) * a.c) * kTile + 64 * pw + (lane % boxes) * a.box;
-          rows = key < n ? entry(b, static_cast<int>(key), n) : -1;
+    if (warp == kEntryWarp) {
+      // Entry `key` of sequence b as a row of the pool, or -1.
+      auto entry = [&](int b, int key, int n) {
+        if (key >= n) return -1;
+        const int pg = a.P > 1 ? static_cast<int>(__umulhi(key, a.p_mul) >> a.p_shift) : key;
+        const int id = a.table[static_cast<size_t>(b) * a.max_pages + pg];
+        return id >= 0 && id < a.N ? id * a.P + (key - pg * a.P) : -1;
+      };
+      // This rank's entry tiles i, i + c, .. of sequence b below n.  The page chunks of
+      // the next 32 / chunks tiles are looked up at once, a lane each; then one
+      // thread walks those tiles (per tile, a warp's lookups, votes and branches paced
+      // the loop at 2000 cycles; these take a few dozen instructions).
+      const int chunks = a.box ? kTile / a.box : 32;
+      const int ahead = a.box ? 32 / chunks : 1;
+      auto put_tiles = [&](int kind, int u, int m, int b, int i, int n) {
+        const int end = static_cast<int>((static_cast<uint32_t>(n) + kTile - 1) / kTile);
+        while (ok && i < end) {
+          const int batch = min(ahead, (end - i + a.c - 1) >> a.log_c);
+          int good = 0;                  // tiles before the first with a missing page
+          if (a.box) {
+            const int t = lane / chunks;
+            const long long key = (i + static_cast<long long>(t) * a.c) * kTile + (lane % chunks) * a.box;
+            const int row = t < batch && key < n ? entry(b, static_cast<int>(key), n) : -1;
+            const uint32_t bad = __ballot_sync(0xffffffffu, t < batch && key < n && row < 0);
+            good = bad ? (__ffs(bad) - 1) / chunks : batch;
+            sm.rows[lane] = row;
+            __syncwarp();
+            bool fine = true;
+            if (elect_one()) {
+              int stage = g % kStages, use = g / kStages, key0 = i * kTile;
+              for (int k = 0; k < good; ++k, key0 += a.c * kTile) {
+                if (use >= 1 && !wait1(&sm.kv_empty[stage], (use - 1) & 1, a, abort_flag, 20)) { fine = false; break; }
+                const int cnt = min(kTile, n - key0);
+                uint4 bits = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+                if (cnt < kTile) {
+                  uint32_t off[4];
+                  lanes_off(off, 0, cnt);
+                  bits = make_uint4(~off[0], ~off[1], ~off[2], ~off[3]);
+                }
+                sm.valid[stage] = bits;
+                sm.desc[stage] = make_desc(kind, u, m, cnt, (key0 / kTile >> a.log_c) & 1);
+                const int boxes = (cnt + a.box - 1) / a.box;
+                mbar_expect_tx(&sm.kv_full[stage], boxes * a.box * kDim * 2);
+                uint32_t dst = smem_u32(sm.kv[stage]);
+                for (int x = 0; x < boxes; ++x, dst += a.box * 128) {
+                  const int y = sm.rows[k * chunks + x];
+                  tma_load_2d(dst, reinterpret_cast<uint64_t>(&pool_map), 0, y, &sm.kv_full[stage]);
+                  tma_load_2d(dst + kRegion, reinterpret_cast<uint64_t>(&pool_map), 64, y, &sm.kv_full[stage]);
+                }
+                mbar_arrive_n(&sm.kv_full[stage], 33);
+                if (++stage == kStages) { stage = 0; ++use; }
+              }
+            }
+            ok = __all_sync(0xffffffffu, fine);
+            g += good;
+            i += good * a.c;
+          }
+          if (ok && good < batch) {
+            const int key0 = i * kTile;
+            put(make_desc(kind, u, m, min(kTile, n - key0), (i >> a.log_c) & 1), a.pool, kTile, [&](int r) { return entry(b, key0 + r, n); });
+            i += a.c;
+          }
         }
-        const int y = __shfl_sync(0xffffffffu, rows, k * boxes + lane % boxes);
-        if (!a.box || key0 + kTile > n || __any_sync(0xffffffffu, y < 0)) {
-          ok = put(d, [&](int r) { return entry(b, key0 + r, n); });
-          continue;
-        }
-        const int stage = g % kStages, use = g / kStages;
-        if (use >= 1 && !waitw(&sm.kv_empty[stage], (use - 1) & 1, a, abort_flag, 20)) { ok = false; break; }
-        if (lane == 0) {
-          announce(stage, d, 0xffffffffu, 0xffffffffu);
-          mbar_arrive_expect_tx(&sm.kv_full[stage], 64 * kDim * 2);
-        }
-        __syncwarp();
-        if (lane < 2 * boxes) {                        // lanes [0, boxes): dims 0 .. 63, the next: 64 .. 127
-          const int h = lane >= boxes ? 1 : 0;
-          tma_load_2d(smem_u32(sm.kv[stage]) + h * kRegion + (64 * pw + (lane - h * boxes) * a.box) * 128,
-                      reinterpret_cast<uint64_t>(&pool_map), 64 * h, y, &sm.kv_full[stage]);
-        }
-        mbar_arrive(&sm.kv_full[stage]);
-#pragma unroll
-        for (int s = 0; s < kStages; ++s)
-          if (s == stage) armed[s] = use;
-        ++g;
+      };
+      put_tiles(kShared, 0, 0, sm.leader, rank, sm.shared * kTile);
+      for (int u = 0; u < sm.npair && ok;) {
+        int m = 1;
+        while (u + m < sm.npair && joined(sm, u + m)) ++m;
+        put_tiles(kOwn, u, m, sm.pair[u].b, own0, sm.pair[u].n);
+        u += m;
       }
-    };
-    put_tiles(kShared, 0, sm.leader, rank, sm.shared * kTile);
-    // the first tile of this rank behind the shared ones
-    const int own0 = sm.shared + (rank - sm.shared % a.c + a.c) % a.c;
-    for (int u = 0; u < sm.npair && ok; ++u) put_tiles(kOwn, u, sm.pair[u].b, own0, sm.pair[u].n);
-    const int segs = a.win_run / 16;
-    if (rank * a.win_run < a.W) {
-      for (int k0 = 0; ok && k0 < sm.npair * segs; k0 += 8)
-        ok = put(Desc{kWindow, 0, min(8, sm.npair * segs - k0), k0}, [&](int r) {
+      for (; ok && g <= entry_tiles + win_tiles; ++g) {
+        if (g < kStages) continue;
+        ok = stage_free();
+        if (ok && lane == 0) mbar_arrive(&sm.win_go[g % kStages]);
+        __syncwarp();
+      }
+      cp_async_wait<0>();
+    } else {
+      for (int t = 0; ok && t < win_tiles; ++t) {
+        const int k0 = 8 * t, runs = min(8, sm.npair * segs - k0);
+        put(make_desc(kWindow, 0, 0, runs, k0), a.kv_raw, runs * 16, [&](int r) {
           const int sg = k0 + (r >> 4), u = sg / segs;
           if (u >= sm.npair) return -1;
           const Pair pr = sm.pair[u];
@@ -513,54 +627,46 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
           const int back = rank * a.win_run + (sg - u * segs) * 16 + (r & 15);
           return back < pr.nw ? pr.b * a.raw_cap + (pr.p - back) % a.raw_cap : -1;
         });
-    }
-    if (ok) put(Desc{kEnd, 0, 0, 0}, [](int) { return -1; });
-    cp_async_wait<0>();
-    if (*abort_flag) {
-      // boxes still in flight land within microseconds
-#pragma unroll
-      for (int s = 0; s < kStages; ++s)
-        if (armed[s] >= 0) drain_wait(&sm.kv_full[s], armed[s] & 1);
+      }
+      if (ok) put(make_desc(kEnd, 0, 0, 0, 0), a.pool, 0, [](int) { return -1; });
+      cp_async_wait<0>();
     }
   } else if (!idle && warp == kQkWarp) {
     // ================================================================= S = Q K^T
     constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0, 0);
-    const uint32_t qb = smem_u32(sm.q);
-    bool ok = waitw(&sm.q_full, 0, a, abort_flag, 21), more = true;
-    int ends = 0;
-    for (int g = 0; ok; ++g) {
-      const int stage = g % kStages, w = g & 1;
-      if (more) {
-        ok = waitw(&sm.kv_full[stage], (g / kStages) & 1, a, abort_flag, 25);
-        if (!ok) break;
-        more = sm.desc[stage].kind != kEnd;
-      }
-      ok = g < 2 || waitw(&sm.s_free[w], ((g >> 1) - 1) & 1, a, abort_flag, 27);
-      if (!ok) break;
-      if (!more) {                 // the end, told to both warpgroups
-        if (elect_one()) {
-          sm.s_stage[w] = -1;
-          mbar_arrive(&sm.s_full[w]);
-          mbar_arrive(&sm.s_full[w]);
-        }
-        __syncwarp();
-        if (++ends == 2) break;
-        continue;
-      }
-      fence_proxy_async();
-      tc_fence_after();
-      const uint32_t kb = smem_u32(sm.kv[stage]), scol = tmem + kColS + 128 * w;
-      if (elect_one()) {
-#pragma unroll
-        for (int j = 0; j < kDim / 16; ++j)
-          mma_bf16(scol, desc_kmajor(qb, j), desc_kmajor(kb, j), idesc_qk, j > 0);
-        tc_commit(&sm.s_full[w]);
-        sm.s_stage[w] = stage;
-        mbar_arrive(&sm.s_full[w]);
-      }
-      __syncwarp();
-    }
     if (elect_one()) {
+      const uint64_t qd = desc_kmajor(smem_u32(sm.q), 0);
+      bool ok = wait1(&sm.q_full, 0, a, abort_flag, 21);
+      int stage = 0, round = 0;
+      for (int g = 0, ends = 0; ok; ++g) {
+        const int w = g & 1;
+        if (!ends) {
+          ok = wait1(&sm.kv_full[stage], round & 1, a, abort_flag, 25);
+          if (!ok) break;
+          ends = sm.desc[stage].kind == kEnd;
+        }
+        ok = g < 2 || wait1(&sm.s_free[w], ((g >> 1) - 1) & 1, a, abort_flag, 27);
+        if (!ok) break;
+        if (ends) {                 // the end, told to both warpgroups
+          if (ends == 1) *const_cast<volatile int*>(&sm.tiles) = g;
+          mbar_arrive_n(&sm.s_full[w], 2);
+          if (++ends == 3) break;
+          continue;
+        }
+        fence_proxy_async();
+        tc_fence_after();
+        const uint64_t kd = desc_kmajor(smem_u32(sm.kv[stage]), 0);
+        const uint32_t scol = tmem + kColS + 128 * w;
+#pragma unroll
+        for (int j = 0; j < kDim / 16; ++j) {
+          // (16 elements on: 32 bytes, or the other 64-dim half)
+          const uint64_t step = ((j >> 2) * kRegion + (j & 3) * 32) >> 4;
+          mma_bf16(scol, qd + step, kd + step, idesc_qk, j > 0);
+        }
+        tc_commit(&sm.s_full[w]);
+        mbar_arrive(&sm.s_full[w]);
+        if (++stage == kStages) { stage = 0; ++round; }
+      }
       tc_commit(&sm.drain[0]);
       drain_wait(&sm.drain[0], 0);
     }
@@ -568,54 +674,54 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   } else if (!idle && warp == kPvWarp) {
     // ================================================================= O += P K
     constexpr uint32_t idesc_pv = idesc_bf16(128, 128, 0, 1);
-    const int segs = max(a.win_run / 16, 1);
     const uint32_t ocol = tmem + kColO;
-    for (int g = 0;; ++g) {
-      const int stage = g % kStages, w = g & 1;
-      if (!waitw(&sm.kv_full[stage], (g / kStages) & 1, a, abort_flag, 28)) break;
-      const Desc d = sm.desc[stage];
-      if (d.kind == kEnd) break;
-      if (!waitw(&sm.p_full[w], (g >> 1) & 1, a, abort_flag, 26)) break;
-      fence_proxy_async();
-      tc_fence_after();
-      const uint32_t kb = smem_u32(sm.kv[stage]), pcol = tmem + kColP + 64 * w;
-      if (d.kind == kShared) {
-        if (elect_one()) {
+    if (elect_one()) {
+      int stage = 0, round = 0;
+      for (int g = 0;; ++g) {
+        const int w = g & 1;
+        if (!wait1(&sm.kv_full[stage], round & 1, a, abort_flag, 28)) break;
+        const Desc d = sm.desc[stage];
+        if (d.kind == kEnd) break;
+        const uint64_t kd = desc_mnmajor(smem_u32(sm.kv[stage]), 0);
+        const uint32_t pcol = tmem + kColP + 64 * w;
+        if (!wait1(&sm.p_full[w], (g >> 1) & 1, a, abort_flag, 26)) break;
+        fence_proxy_async();
+        tc_fence_after();
+        if (d.kind == kShared) {
 #pragma unroll
-          for (int j = 0; j < kTile / 16; ++j) mma_ts(ocol, pcol + 8 * j, desc_mnmajor(kb, j), idesc_pv);
-          tc_commit(&sm.kv_empty[stage]);
-          tc_commit(&sm.pv_done[w]);
-        }
-      } else if (elect_one()) {
-        int u = d.kind == kWindow ? d.seg0 / segs : d.u;
-        int left = d.kind == kWindow ? segs - d.seg0 % segs : kTile;
-        uint32_t off[4];
-        lanes_off(off, u * a.H, u * a.H + a.H);
-        for (int j = 0; j < d.nk; ++j) {
-          mma_ts_lanes(ocol, pcol + 8 * j, desc_mnmajor(kb, j), idesc_pv, off);
-          if (--left == 0) {        // the next run is the next pair's
-            ++u;
-            left = segs;
-            lanes_off(off, u * a.H, u * a.H + a.H);
+          for (int j = 0; j < kTile / 16; ++j) mma_ts(ocol, pcol + 8 * j, kd + j * (2048 >> 4), idesc_pv);
+        } else {
+          const bool win = d.kind == kWindow;
+          const int steps = win ? d.cnt : (d.cnt + 15) / 16, m = win ? 1 : d.m();
+          int u = win ? d.seg0 / segs : d.u();
+          int left = win ? segs - d.seg0 % segs : kTile;
+          uint32_t off[4];
+          lanes_off(off, u * a.H, (u + m) * a.H);
+          for (int j = 0; j < steps; ++j) {
+            mma_ts_lanes(ocol, pcol + 8 * j, kd + j * (2048 >> 4), idesc_pv, off);
+            if (--left == 0) {        // the next run is the next pair's
+              ++u;
+              left = segs;
+              lanes_off(off, u * a.H, (u + m) * a.H);
+            }
           }
         }
         tc_commit(&sm.kv_empty[stage]);
         tc_commit(&sm.pv_done[w]);
+        if (++stage == kStages) { stage = 0; ++round; }
       }
-      __syncwarp();
-    }
-    // whatever was issued has finished before O is read and tensor memory released
-    if (elect_one()) {
+      // whatever was issued has finished before O is read and tensor memory released
       tc_commit(&sm.drain[1]);
       drain_wait(&sm.drain[1], 0);
     }
     __syncwarp();
-  } else if (!idle && warp < kProd0) {
-    // ================================================================= softmax, tiles g % 2 == w
+  } else if (!idle && warp < kSoftWarps) {
+    // ================================================================= softmax
+    // tiles g % 2 == w
     const int w = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t scol = tmem + lane_addr + kColS + 128 * w, pcol = tmem + lane_addr + kColP + 64 * w;
-    const uint32_t ocol = tmem + lane_addr + kColO;
+    const uint32_t ocol = tmem + lane_addr + kColO + 64 * w;      // (to be cleared)
     const int rows = sm.npair * a.H;
     {
       // Q: 16 lanes a row; rows beyond the job's are zero
@@ -623,43 +729,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       const uint32_t dst = smem_u32(sm.q) + (c >> 3) * kRegion;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + c * 8;
 #pragma unroll
-      for (int i = 0; i < kTile / 16; ++i) {
-        const int x = (threadIdx.x >> 4) + 16 * i;
-        const int ux = static_cast<int>((static_cast<uint32_t>(x) * a.h_inv) >> 16);
+      for (int i = 0; i < kTile / kSoftWarps / 2; ++i) {
+        const int y = (threadIdx.x >> 4) + 2 * kSoftWarps * i;
+        const int uy = static_cast<int>((static_cast<uint32_t>(y) * a.h_inv) >> 16);
         size_t row = 0;
-        bool some = x < rows;
+        bool some = y < rows;
         if (some) {
-          const int b = sm.pair[ux].b;
+          const int b = sm.pair[uy].b;
           some = b >= 0;
-          row = (static_cast<size_t>(max(b, 0)) * a.T + sm.pair[ux].t) * a.H + (x - ux * a.H);
+          row = (static_cast<size_t>(max(b, 0)) * a.T + sm.pair[uy].t) * a.H + (y - uy * a.H);
         }
-        cp_async16(dst + x * 128 + (((c & 7) ^ (x & 7)) << 4), q + row * kDim, some ? 16u : 0u);
+        cp_async16(dst + y * 128 + (((c & 7) ^ (y & 7)) << 4), q + row * kDim, some ? 16u : 0u);
       }
       cp_async_commit();
       uint32_t z[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) z[e] = 0u;
 #pragma unroll
-      for (int cc = 0; cc < 64; cc += 16) tmem_st16(ocol + 64 * w + cc, z);
+      for (int cc = 0; cc < 64; cc += 16) tmem_st16(ocol + cc, z);
       tmem_st_wait();
       tc_fence_before();
+      hand_over(&sm.m_next[w][r], -1, -INFINITY);
+      hand_over(&sm.l_sum[w][r], -1, 0.f);
+      if (w == 0) sm.redo[r] = 0;
       cp_async_wait<0>();
       if (a.negate) {
-        for (int i = 0; i < kTile / 16; ++i) {
-          const int x = (threadIdx.x >> 4) + 16 * i;
-          uint4* v = reinterpret_cast<uint4*>(sm.q + (c >> 3) * kRegion + x * 128 + (((c & 7) ^ (x & 7)) << 4));
+        for (int i = 0; i < kTile / kSoftWarps / 2; ++i) {
+          const int y = (threadIdx.x >> 4) + 2 * kSoftWarps * i;
+          uint4* v = reinterpret_cast<uint4*>(sm.q + (c >> 3) * kRegion + y * 128 + (((c & 7) ^ (y & 7)) << 4));
           *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
         }
       }
-      hand_over(&sm.m_next[w][r], -1, -INFINITY);
-      hand_over(&sm.l_next[w][r], -1, 0.f);
       fence_proxy_async();
       mbar_arrive(&sm.q_full);
     }
     const int u = r < rows ? static_cast<int>((static_cast<uint32_t>(r) * a.h_inv) >> 16) : -1;
-    const int segs = max(a.win_run / 16, 1);
     const float sl2 = a.scale_log2;
-    for (int g = w;; g += 2) {
+    const int shared_tiles = tiles_of(rank, sm.shared * kTile, a.log_c);
+    float M = -INFINITY, l = 0.f;      // -inf: not set yet
+    bool first_known = false;
+    int stage = w;                       // g % kStages
+    for (int g = w;; g += 2, stage = stage + 2 >= kStages ? stage + 2 - kStages : stage + 2) {
       const int k = g >> 1;
       if (!waitw(&sm.s_full[w], k & 1, a, abort_flag, 22)) break;
       tc_fence_after();
@@ -669,87 +779,76 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       PA_TMEM_LD_X32(scol + 32, v + 32);
       PA_TMEM_LD_X32(scol + 64, v + 64);
       PA_TMEM_LD_X32(scol + 96, v + 96);
-      const int stage = sm.s_stage[w];
-      const Desc d = sm.desc[max(stage, 0)];
-      uint32_t see[4];
+      const bool end = g >= *const_cast<volatile int*>(&sm.tiles);
+      const Desc d = sm.desc[stage];
+      const uint4 bits = sm.valid[stage];
       bool mine = d.kind == kShared;       // the tile's MMA writes this row's lane
       int lo = 0, hi = kTile;
       if (d.kind == kOwn) {
-        mine = u == d.u;
+        mine = u >= d.u() && u < d.u() + d.m();
       } else if (d.kind == kWindow) {
         lo = min(max(u * segs - d.seg0, 0), 8) * 16;
         hi = min(max((u + 1) * segs - d.seg0, 0), 8) * 16;
         mine = u >= 0 && hi > lo;
       }
-      bool full = d.kind != kWindow;       // every row that counts sees every column
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        see[i] = sm.valid[max(stage, 0)][i];
-        full = full && see[i] == 0xffffffffu;
-      }
+      const bool full = d.kind == kShared && (bits.x & bits.y & bits.z & bits.w) == 0xffffffffu;
       const bool any = __any_sync(0xffffffffu, mine);
       tmem_ld_wait();
-      if (stage < 0) break;
+      if (end) break;
       tc_fence_before();
       mbar_arrive(&sm.s_free[w]);
-      float mx = -INFINITY;
-      if (any) {
-        if (!full) {
-          uint32_t off[4];
-          lanes_off(off, lo, hi);
+      if (any && !full) {
+        uint32_t off[4];
+        lanes_off(off, lo, hi);
+        const uint32_t see[4] = {mine ? bits.x & ~off[0] : 0u, mine ? bits.y & ~off[1] : 0u,
+                                 mine ? bits.z & ~off[2] : 0u, mine ? bits.w & ~off[3] : 0u};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) see[i] = mine ? see[i] & ~off[i] : 0u;
-#pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (!((see[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;   // -inf: weight 0
-        }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < 128; e += 2) mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-        mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], -INFINITY) * sl2;   // NaN if there is one
-        if (!mine) mx = -INFINITY;
+        for (int e = 0; e < 128; ++e)
+          if (!((see[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;   // -inf: weight 0
       }
-      // M as the tile before left it, then as this one does
-      float Mp = -INFINITY;
-      if (g > 0 && !take(&sm.m_next[w ^ 1][r], g - 1, &Mp, a, abort_flag, 23)) break;
-      const bool move = Mp > -INFINITY && mx > Mp + kLazy;
-      const float Mn = Mp == -INFINITY || move ? fmaxf(mx, Mp) : Mp;
-      hand_over(&sm.m_next[w][r], g, Mn);
-      if (__any_sync(0xffffffffu, move)) {
-        // O moves to the new M: behind the PV of the tile before, ahead of this one's
-        if (!waitw(&sm.pv_done[w ^ 1], ((g - 1) >> 1) & 1, a, abort_flag, 24)) break;
-        tc_fence_after();
-        const float f = move ? ex2(Mp - Mn) : 1.f;
-#pragma unroll 1
-        for (int cc = 0; cc < kDim; cc += 8) {
-          uint32_t o[8];
-          PA_TMEM_LD_X8(ocol + cc, o);
-          tmem_ld_wait();
+      // Where the rank has shared tiles, the first sets every row's M; else a row's comes
+      // with its first own tile, and whatever is set goes along from tile to tile.
+      if (!first_known) {
+        if (g > 0 && !take(&sm.m_next[w ^ 1][r], g - 1, &M, a, abort_flag, 23)) break;
+        const bool sets = mine && M == -INFINITY;
+        if (__any_sync(0xffffffffu, sets)) {
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          PA_TMEM_ST_X8(ocol + cc, o);
+          for (int e = 0; e < 128; e += 2)
+            mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], -INFINITY) * sl2;   // (NaN stays)
+          if (sets) M = mx == -INFINITY ? 0.f : mx;
         }
-        tmem_st_wait();
+        hand_over(&sm.m_next[w][r], g, M);
+        first_known = rank < sm.shared;
       }
       // P's buffer is free once the PV two tiles back has read it
       if (g >= 2 && !waitw(&sm.pv_done[w], (k - 1) & 1, a, abort_flag, 29)) break;
       tc_fence_after();
+      if (d.kind == kOwn && (d.cnt & 15)) {
+        // the tile's rows behind the last key, in its 16: P is 0 there, but what the page
+        // holds may be NaN
+        for (int i = d.cnt * 16 + (threadIdx.x & 127); i < (d.cnt + 15) / 16 * 256; i += 128)
+          *reinterpret_cast<uint4*>(sm.kv[stage] + ((i >> 3) & 1) * kRegion + (i >> 4) * 128 +
+                                    (((i & 7) ^ ((i >> 4) & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();
+      }
       float sum = 0.f;
       if (any) {
-        const float negM = Mn > -INFINITY ? -Mn : 0.f;
+        const float negM = M == -INFINITY ? 0.f : -M;
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
         for (int cc = 0; cc < 128; cc += 32) {
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x0, x1;
-            fma2(x0, x1, __uint_as_float(v[cc + e]), __uint_as_float(v[cc + e + 1]), sl2, negM);
-            x0 = ex2(x0);
-            x1 = ex2(x1);
-            if (e & 2) add2(s0, s1, x0, x1);
-            else add2(s2, s3, x0, x1);
+          for (int e = 0; e < 32; e += 4) {
+            const float x0 = ex2(fmaf(__uint_as_float(v[cc + e]), sl2, negM));
+            const float x1 = ex2(fmaf(__uint_as_float(v[cc + e + 1]), sl2, negM));
+            const float x2 = ex2(fmaf(__uint_as_float(v[cc + e + 2]), sl2, negM));
+            const float x3 = ex2(fmaf(__uint_as_float(v[cc + e + 3]), sl2, negM));
+            s0 += x0; s1 += x1; s2 += x2; s3 += x3;
             pk[e >> 1] = pack_bf16(x0, x1);
+            pk[(e >> 1) + 1] = pack_bf16(x2, x3);
           }
           tmem_st16(pcol + (cc >> 1), pk);
         }
@@ -758,28 +857,44 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       }
       tc_fence_before();
       mbar_arrive(&sm.p_full[w]);
-      // l goes from tile to tile as M does, in the order of the tiles
-      float l = 0.f;
-      if (g > 0 && !take(&sm.l_next[w ^ 1][r], g - 1, &l, a, abort_flag, 30)) break;
-      if (Mp != Mn) l *= ex2(Mp - Mn);
-      hand_over(&sm.l_next[w][r], g, l + sum);
+      if (sum > kMost) sm.redo[r] = 1;
+      // Row sums.  Shared tile g belongs to parity g % 2, so each warpgroup has
+      // its own; behind them a tile may come to either, and both go along.
+      if (d.kind == kShared) {
+        l += sum;
+        hand_over(&sm.l_sum[w][r], g, l);
+      } else {
+        float own = l, other = 0.f;
+        if (g > 0) {
+          if (!take(&sm.l_sum[w ^ 1][r], g - 1, &other, a, abort_flag, 30)) break;
+          if (g > shared_tiles && !take(&sm.l_sum[w][r], g - 1, &own, a, abort_flag, 33)) break;
+        }
+        // an own tile's parity, the window's is 1
+        const int p = d.kind == kOwn ? d.seg0 : 1;
+        if (p == w) own += sum; else other += sum;
+        hand_over(&sm.l_sum[w ^ 1][r], g, other);
+        hand_over(&sm.l_sum[w][r], g, own);
+      }
     }
   }
   __syncthreads();
-  if (!idle && warp < kProd0) {
-    // The last tile's M and l hold for O.  Warpgroup w moves dims [64 w, 64 w + 64) of
-    // O to where the key tiles were.
+  if (*abort_flag) {
+    // boxes still in flight land within microseconds
+    for (const uint64_t t0 = global_ns(); global_ns() - t0 < 200000ull;) {}
+  } else if (!idle && warp < kSoftWarps) {
+    // Warpgroup w moves dims [64 w, 64 w + 64) of O to where the key tiles were.
     const int w = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t ocol = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO + 64 * w;
     if (w == 0) {
-      int t0, t1, t2;
-      const float m0 = handed(&sm.m_next[0][r], &t0), m1 = handed(&sm.m_next[1][r], &t1);
-      sm.m[r] = t1 > t0 ? m1 : m0;
-      sm.l[r] = handed(&sm.l_next[t1 > t0 ? 1 : 0][r], &t2);
+      int t;
+      // (a row's M is set once: whichever parity has it, the other has it or nothing)
+      const float m0 = handed(&sm.m_next[0][r], &t), m1 = handed(&sm.m_next[1][r], &t);
+      sm.m[r] = m0 == -INFINITY ? m1 : m0;
+      sm.l[r] = handed(&sm.l_sum[0][r], &t) + handed(&sm.l_sum[1][r], &t);
     }
     uint8_t* dst = &sm.kv[0][0] + r * (kDim * 4);
     tc_fence_after();
     uint32_t x[64];
+    const uint32_t ocol = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO + 64 * w;
     PA_TMEM_LD_X32(ocol, x);
     PA_TMEM_LD_X32(ocol + 32, x + 32);
     tmem_ld_wait();
@@ -787,77 +902,100 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     for (int e = 0; e < 64; e += 4)
       *reinterpret_cast<uint4*>(dst + ((((64 * w + e) >> 2) ^ lane) << 4)) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
   }
+  // The ranks' parts of a row meet at the rank that owns it (128 / c rows each): every
+  // rank pushes 16-byte-aligned row blocks to the others (pulling them with loads
+  // from distributed shared memory took three times as long).
+  const int per = kTile / a.c, row0 = rank * per;
+  uint8_t* const parts = &sm.kv[2][0];
+  if (threadIdx.x == 0) mbar_arrive_expect_tx(&sm.joined, (a.c - 1) * per * kDim * 4);
   tc_fence_before();
+  fence_proxy_async();
   cluster_arrive();
   cluster_wait();
-  // Each rank finishes every c-th row: a warp a row, a lane 4 dims.  Three rows' parts
-  // from every rank are on their way before the first is used.
-  constexpr int kFly = 3;
   const bool finish = !idle && !*abort_flag;
-  const int step = a.c * (kThreads / 32), rows_all = idle ? 0 : sm.npair * a.H;
-  for (int r0 = rank + a.c * warp; finish && r0 < rows_all; r0 += kFly * step) {
-    float4 o[kFly][kMaxCluster];
-    float mi[kFly], li[kFly];
-#pragma unroll
-    for (int x = 0; x < kFly; ++x) {
-      const int r = min(r0 + x * step, rows_all - 1);
-      const float* orow = reinterpret_cast<const float*>(&sm.kv[0][0] + r * (kDim * 4) + ((lane ^ (r & 31)) << 4));
-      mi[x] = -INFINITY;
-      li[x] = 0.f;
-      if (lane < a.c) {
-        mi[x] = ld_peer(peer_addr(&sm.m[r], lane));
-        li[x] = ld_peer(peer_addr(&sm.l[r], lane));
-      }
-#pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k)
-        if (k < a.c) o[x][k] = ld_peer4(peer_addr(orow, k));
-    }
-#pragma unroll
-    for (int x = 0; x < kFly; ++x) {
-      const int r = r0 + x * step;
-      const int u = static_cast<int>((static_cast<uint32_t>(r) * a.h_inv) >> 16);
-      if (r >= rows_all) continue;
-      const Pair pr = sm.pair[u];
-      if (pr.b < 0) continue;
-      float M = mi[x];
-#pragma unroll
-      for (int y = 4; y > 0; y >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
-      M = __shfl_sync(0xffffffffu, M, 0);
-      const float fi = mi[x] > -INFINITY ? ex2(mi[x] - M) : 0.f;
-      float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k) {
-        if (k >= a.c) break;
-        const float f = __shfl_sync(0xffffffffu, fi, k), lk = __shfl_sync(0xffffffffu, li[x], k);
-        L = fmaf(f, lk, L);
-        acc[0] = fmaf(f, o[x][k].x, acc[0]);
-        acc[1] = fmaf(f, o[x][k].y, acc[1]);
-        acc[2] = fmaf(f, o[x][k].z, acc[2]);
-        acc[3] = fmaf(f, o[x][k].w, acc[3]);
-      }
-      const int h = r - u * a.H;
-      const size_t row = (static_cast<size_t>(pr.b) * a.T + pr.t) * a.H + h;
-      float sc = 0.f, lse = -INFINITY;
-      if (L != 0.f) {
-        const float sg = sm.sink_l2[h];
-        const float X = fmaxf(M, sg), fm = ex2(M - X);
-        sc = __fdiv_rn(fm, fmaf(L, fm, ex2(sg - X)));
-        lse = (M + log2f(L)) * 0.6931471805599453f;
-      }
-      uint2 o2;
-      o2.x = pack_bf16(acc[0] * sc, acc[1] * sc);
-      o2.y = pack_bf16(acc[2] * sc, acc[3] * sc);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kDim + lane * 4) = o2;
-      if (a.lse && lane == 0) a.lse[row] = lse;
+  const int rows_all = idle ? 0 : sm.npair * a.H;
+  if (finish && warp == 0 && elect_one()) {
+    for (int k = 1; k < a.c; ++k) {
+      const int to = (rank + k) & (a.c - 1);
+      push_to_peer(peer_addr(parts + rank * (per * kDim * 4), to), &sm.kv[0][0] + to * (per * kDim * 4), per * kDim * 4,
+                   peer_addr(&sm.joined, to));
     }
   }
   __syncwarp();
-  cluster_arrive();        // peers may not leave before their rows are read
+  // A warp finishes rows row0 + warp + 12 n, n < 11.  Lane n c + k first gets rank k's
+  // (M, l) of row n; what a row needs of them is worked out for all rows at once.
+  constexpr int kWarps = kThreads / 32;
+  const int n_of = lane >> a.log_c, k_of = lane & (a.c - 1);
+  const int r_of = row0 + warp + kWarps * n_of;
+  const bool counts = finish && warp + kWarps * n_of < per && r_of < rows_all;
+  float mi = -INFINITY, li = 0.f;
+  bool again = false;
+  int h_of = 0;
+  size_t row_of = 0;
+  bool real = false;
+  if (counts) {
+    mi = ld_peer(peer_addr(&sm.m[r_of], k_of));
+    li = ld_peer(peer_addr(&sm.l[r_of], k_of));
+    again = ld_peer_u8(peer_addr(&sm.redo[r_of], k_of)) != 0;
+    const int u = static_cast<int>((static_cast<uint32_t>(r_of) * a.h_inv) >> 16);
+    h_of = r_of - u * a.H;
+    real = sm.pair[u].b >= 0;
+    if (real) row_of = (static_cast<size_t>(sm.pair[u].b) * a.T + sm.pair[u].t) * a.H + h_of;
+  }
+  float M = mi;
+  for (int y = 1; y < a.c; y <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
+  float fi = mi == -INFINITY ? 0.f : ex2(mi - M);
+  float L = fi * li;
+  for (int y = 1; y < a.c; y <<= 1) L += __shfl_xor_sync(0xffffffffu, L, y);
+  float lse = -INFINITY, sc = 0.f;
+  if (L != 0.f) {
+    const float sg = sm.sink_l2[h_of], X = fmaxf(M, sg), fm = ex2(M - X);
+    sc = __fdiv_rn(fm, fmaf(L, fm, ex2(sg - X)));
+    lse = (M + log2f(L)) * 0.6931471805599453f;
+  }
+  const uint32_t redo_lanes = __ballot_sync(0xffffffffu, real && again);
+  bool there = finish;
+  if (finish && a.c > 1) there = waitw(&sm.joined, 0, a, abort_flag, 34);
+  for (int n = 0, i = warp; there && i < per && row0 + i < rows_all; ++n, i += kWarps) {
+    const int r = row0 + i, src = n << a.log_c;
+    const size_t row = __shfl_sync(0xffffffffu, row_of, src);
+    if (!__shfl_sync(0xffffffffu, static_cast<int>(real), src)) continue;
+    if ((redo_lanes >> src) & ((1u << a.c) - 1u)) continue;       // done again below
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint32_t at = (lane ^ (r & 31)) << 4;
+    for (int k = 0; k < a.c; ++k) {
+      const float f = __shfl_sync(0xffffffffu, fi, src + k);
+      const uint8_t* part = k == rank ? &sm.kv[0][0] + r * (kDim * 4) : parts + (k * per + i) * (kDim * 4);
+      const float4 o = *reinterpret_cast<const float4*>(part + at);
+      acc[0] = fmaf(f, o.x, acc[0]);
+      acc[1] = fmaf(f, o.y, acc[1]);
+      acc[2] = fmaf(f, o.z, acc[2]);
+      acc[3] = fmaf(f, o.w, acc[3]);
+    }
+    const float scr = __shfl_sync(0xffffffffu, sc, src);
+    uint2 o2;
+    o2.x = pack_bf16(acc[0] * scr, acc[1] * scr);
+    o2.y = pack_bf16(acc[2] * scr, acc[3] * scr);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kDim + lane * 4) = o2;
+  }
+  if (there && real && !again && k_of == 0 && a.lse && !((redo_lanes >> lane) & ((1u << a.c) - 1u))) a.lse[row_of] = lse;
+  // (a push that a peer gave up waiting for must not outlive the peer)
+  if (finish && !there)
+    for (const uint64_t t0 = global_ns(); global_ns() - t0 < 200000ull;) {}
+  __syncwarp();
+  cluster_arrive();        // peers may not leave before their parts are read
   if (warp == kQkWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
   cluster_wait();
+  // Rows whose weights left the range, one after the other.
+  for (uint32_t todo = there ? redo_lanes : 0u; todo;) {
+    const int n = (__ffs(todo) - 1) >> a.log_c, r = row0 + warp + kWarps * n;
+    todo &= ~(((1u << a.c) - 1u) << (n << a.log_c));
+    const int u = static_cast<int>((static_cast<uint32_t>(r) * a.h_inv) >> 16);
+    row_exact(a, sm.pair[u], r - u * a.H, sm.sink_l2[r - u * a.H]);
+  }
 }
 
 // The pool as rows of 128 bf16, in boxes of 64 dims with a 128-byte swizzle.
@@ -890,9 +1028,9 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   a.scale_log2 = fmaxf(fabsf(base.tau) * 1.4426950408889634f, 1.17549435e-38f);
   a.negate = base.tau < 0.f;
   a.h_inv = (65536u + a.H - 1) / a.H;
-  // TMA boxes: the largest power of two of rows (8, a swizzle atom, to a warp's 64) in a page
+  // TMA boxes: the largest power of two of rows (8, a swizzle atom, to a tile's 128) in a page
   a.box = a.P & -a.P;
-  a.box = a.box > 64 ? 64 : a.box < 8 ? 0 : a.box;
+  a.box = a.box > kTile ? kTile : a.box < 8 ? 0 : a.box;
   CUtensorMap map = {};
   if (a.N == 0) a.box = 0;
   if (a.box && !make_pool_map(&map, a.pool, static_cast<uint64_t>(a.N) * a.P, a.box)) return CSA_ERR_CUDA;
@@ -903,6 +1041,11 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   const long long tiles = (static_cast<long long>(a.max_pages) * a.P + kTile - 1) / kTile;
   a.c = tiles < 8 ? 1 : tiles < 16 ? 2 : tiles < 128 ? 4 : 8;
   if (const char* e = getenv("PA_C")) a.c = atoi(e);
+  a.log_c = 31 - __builtin_clz(static_cast<unsigned>(a.c));
+  // The round-up reciprocal of P for 31-bit numerators: with 2^s the power of two at or
+  // above P, ceil(2^(31 + s) / P) fits 32 bits and errs by less than 2^s.
+  a.p_shift = a.P > 1 ? 31 - __builtin_clz(static_cast<unsigned>(a.P - 1)) : 0;      // s - 1
+  a.p_mul = a.P > 1 ? static_cast<uint32_t>(((1ull << (32 + a.p_shift)) + a.P - 1) / a.P) : 0;
   a.win_run = ((a.W + a.c - 1) / a.c + 15) / 16 * 16;
   int dev = 0;
   cudaGetDevice(&dev);

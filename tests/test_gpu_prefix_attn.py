@@ -91,7 +91,7 @@ class Batch:
                 if len(k) == 0:
                     assert (got == 0).all() and (np64(lse[b, t]) == -np.inf).all()
                     continue
-                e = (self.D + 4) * u * (np.abs(q) @ np.abs(k).T).max() * self.tau + 8 * u * np.abs(rl).max()
+                e = (self.D + 4) * u * (np.abs(q) @ np.abs(k).T).max() * abs(self.tau) + 8 * u * np.abs(rl).max()
                 d = e + 8 * u + (2.0 ** -8 if self.dt == "bf16" else 0.0)
                 tol = (2.05 * d * spread + 2.05 * d * np.abs(ref) * (self.sink is not None)
                        + (len(k) + 16) * u * np.abs(k).max() + torch.finfo(DT[self.dt]).eps / 2 * np.abs(ref) * 1.01)
@@ -212,6 +212,20 @@ def test_bad_pages_are_skipped(mods, dt):
     out, lse = b.run(mods)
     b.keys = lambda i, t: keys[i]
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("tau_sign", [1, -1])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_logits_that_grow_by_hundreds(mods, dt, tau_sign):
+    """A key far behind the first outweighs all before it by e^500 for one head
+    (and is outweighed for the others); so does a window token."""
+    b = Batch([([0, 1, 2], 256)], [700, 260, 300], 1, 16, 128, 128, 64, 40, dt, seed=7, scale=4.0)
+    b.tau *= tau_sign
+    b.pool[b.rows[0][600 // 64], 600 % 64] = 3.0 * tau_sign * b.q[0, 0, 5]
+    b.ring[1, b.pos[1] % b.cap] = 3.0 * tau_sign * b.q[1, 0, 9]
+    out, lse = b.run(mods)
+    b.check(out, lse)
+    assert lse[0, 0, 5] > 400 and lse[1, 0, 9] > 400
 
 
 def test_captured_in_a_graph_and_without_lse(mods):
