@@ -445,7 +445,7 @@ int qk_norm_rope(const void* q, int64_t q_bstride, int64_t q_tstride,
  * over calls in any way gives the same bits.  Sequences with pos0 < 0 or no
  * tokens only copy their carry.
  * pool is one layer [N, P, D] of the inputs' dtype.  Requires D in {64, 128,
- * 256}, m >= 1, P >= 1, 16-byte aligned tensors.
+ * 256}, 1 <= m <= 65536, T <= 2^30, P >= 1, 16-byte aligned tensors.
  */
 int hca_paged_append(const void* a, const void* z, int dtype, int B, int T,
                      int D, int m, const int32_t* pos0, const int32_t* lens,

@@ -8,9 +8,10 @@
 // order.  So a token sequence gives the same bits however calls split it, and the
 // runs of a block are summed in parallel.
 //
-// Bound by HBM: a and z are read once.  D / 8 lanes hold a row (16-byte loads of
-// bf16) and a thread walks the 16 tokens of one run, all of whose loads are
-// independent of its arithmetic.
+// Bound by HBM: a and z are read once.  D / 4 lanes hold a row and a thread walks the
+// 16 tokens of one run, four tokens of loads ahead of its arithmetic (2 x 128K tokens
+// of 128 channels: 3.9 TB/s, against 6.6 for a copy; ten instructions a value and
+// the joins at the end of each block share the SM with the loads).
 #include <cfloat>
 
 #include "rope.cuh"
@@ -18,7 +19,11 @@
 namespace csa {
 
 constexpr int kRun = 16;     // tokens per run
-constexpr int kSlots = 8;    // runs (of one or more blocks) a CTA sums at once
+// Runs (of one or more blocks) a CTA sums at once, and threads an SM holds at least: small
+// CTAs, whose sums and joins overlap each other's (for 2 x 128K tokens 35.7 us with
+// 8 runs, 32.6 us with 4; 512 or 1024 threads an SM: 39.9, 37.3 us).
+constexpr int kSlots = 4;
+constexpr int kSmThreads = 768;
 
 struct AppendArgs {
   const void* a;
@@ -36,112 +41,218 @@ struct AppendArgs {
   float eps;
   int T, m, N, P, max_pages, R, flags;
   int runs;          // per block
-  int sg;            // slots per block
   int ctas_seq;      // CTAs per sequence: one for its first and last blocks, the rest for those between
 };
 
-struct State8 {
-  float M[8], Z[8], A[8];
-};
-__device__ __forceinline__ void empty_state(State8& s) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c) { s.M[c] = -FLT_MAX; s.Z[c] = 0.f; s.A[c] = 0.f; }
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
-// One more token.  A gate of -inf has weight 0; the larger of M and z keeps weight 1,
-// so one exponential serves both.
-__device__ __forceinline__ void add_token(float& M, float& Z, float& A, float z, float a) {
-  const float d = z - M;
-  const float e = expf(-fabsf(d));
-  const bool up = d > 0.f;
-  const float keep = up ? e : 1.f, w = up ? 1.f : e;
-  Z = fmaf(Z, keep, w);
-  // a dropped token's value (weight 0) is not looked at
-  A = fmaf(A, keep, w > 0.f ? w * a : (w == 0.f ? 0.f : w));
-  M = up ? z : M;
+// A thread sums 4 channels: 8 would need twice the registers that let 768 threads
+// share an SM.
+struct State4 {
+  float M[4], Z[4], A[4];
+};
+__device__ __forceinline__ void empty_state(State4& s) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) { s.M[c] = -FLT_MAX; s.Z[c] = 0.f; s.A[c] = 0.f; }
+}
+__device__ __forceinline__ void load4(const float* p, float v[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+// 4 values as loaded (read once: they bypass L1).
+template <typename T> struct Raw4;
+template <> struct Raw4<float> {
+  float4 x;
+  __device__ __forceinline__ void load(const float* p) { x = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void get(float v[4]) const { v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; }
+};
+template <> struct Raw4<__nv_bfloat16> {
+  uint2 x;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = __ldcs(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void get(float v[4]) const {
+    v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
+  }
+};
+__device__ __forceinline__ void store4(float* p, const float v[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+// (d0, d1) = (a0, a1) * (b0, b1) + (c0, c1) on the packed fp32 pipe
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// One more token, two channels.  The larger of M and z keeps weight 1, so one
+// exponential serves both.  A gate of -inf has weight 0; what its token's value
+// may then do to A (0 * inf) is seen to once a run, by the careful form, which does
+// not look at it.
+template <bool CAREFUL>
+__device__ __forceinline__ void add_token2(float* M, float* Z, float* A, const float* z, const float* a) {
+  float d[2], keep[2], w[2], wa[2];
+  fma2(d[0], d[1], M[0], M[1], -1.f, -1.f, z[0], z[1]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float e = exp2_fast(fabsf(d[i]) * -kLog2e);
+    const bool up = d[i] > 0.f;
+    keep[i] = up ? e : 1.f;
+    w[i] = up ? 1.f : e;
+    M[i] = up ? z[i] : M[i];
+  }
+  fma2(Z[0], Z[1], Z[0], Z[1], keep[0], keep[1], w[0], w[1]);
+  mul2(wa[0], wa[1], w[0], w[1], a[0], a[1]);
+  if (CAREFUL) {
+    wa[0] = w[0] == 0.f ? 0.f : wa[0];
+    wa[1] = w[1] == 0.f ? 0.f : wa[1];
+  }
+  fma2(A[0], A[1], A[0], A[1], keep[0], keep[1], wa[0], wa[1]);
 }
 __device__ __forceinline__ void join(float& M, float& Z, float& A, float m2, float z2, float a2) {
   const float mx = fmaxf(M, m2);
-  const float e1 = expf(M - mx), e2 = expf(m2 - mx);
+  const float e1 = exp2_fast((M - mx) * kLog2e), e2 = exp2_fast((m2 - mx) * kLog2e);
   Z = fmaf(Z, e1, z2 * e2);
   A = fmaf(A, e1, a2 * e2);
   M = mx;
 }
 
+// One token after the other.
+template <typename T_, int D, bool CAREFUL>
+__device__ __forceinline__ void add_tokens(State4& st, const T_* z, const T_* a, int t0, int t1) {
+#pragma unroll 1
+  for (int t = t0; t < t1; ++t) {
+    float z4[4], a4[4];
+    Raw4<T_> zr, ar;
+    zr.load(z + static_cast<size_t>(t) * D);
+    ar.load(a + static_cast<size_t>(t) * D);
+    zr.get(z4);
+    ar.get(a4);
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) add_token2<CAREFUL>(st.M + c, st.Z + c, st.A + c, z4 + c, a4 + c);
+  }
+}
+// A whole run: the next kAhead tokens are on their way while these are added.
+constexpr int kAhead = 4;
 template <typename T_, int D>
-__global__ void __launch_bounds__(kSlots * D / 8) append_kernel(const AppendArgs a) {
-  constexpr int G = D / 8;
+__device__ __forceinline__ void add_run(State4& st, const T_* z, const T_* a) {
+  Raw4<T_> zr[2][kAhead], ar[2][kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) { zr[0][i].load(z + i * D); ar[0][i].load(a + i * D); }
+#pragma unroll
+  for (int k = 0; k < kRun / kAhead; ++k) {
+    if (k + 1 < kRun / kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        zr[(k + 1) & 1][i].load(z + ((k + 1) * kAhead + i) * D);
+        ar[(k + 1) & 1][i].load(a + ((k + 1) * kAhead + i) * D);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      float z4[4], a4[4];
+      zr[k & 1][i].get(z4);
+      ar[k & 1][i].get(a4);
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) add_token2<false>(st.M + c, st.Z + c, st.A + c, z4 + c, a4 + c);
+    }
+  }
+}
+
+// E blocks a CTA, kSlots / E runs of each at once.
+template <typename T_, int D, int E>
+__global__ void __launch_bounds__(kSlots * D / 4, kSmThreads / (kSlots * D / 4)) append_kernel(const AppendArgs a) {
+  constexpr int G = D / 8, L = D / 4, SG = kSlots / E;
   __shared__ float part[kSlots][3][D];
-  __shared__ float entry[kSlots][D];
-  __shared__ float2 cs[kSlots][D / 2];
+  __shared__ float entry[E][D];
   const int b = blockIdx.x / a.ctas_seq, job = blockIdx.x - b * a.ctas_seq;
-  const int slot = threadIdx.x / G, l = threadIdx.x % G;   // loading: a run's slot, 8 channels
-  const int ch = threadIdx.x;                              // folding: one channel
-  const long long p0 = a.pos0[b];
-  const int len = p0 < 0 ? 0 : (a.lens ? min(max(a.lens[b], 0), a.T) : a.T);
+  const int slot = threadIdx.x / L, q = threadIdx.x % L;   // summing: a run's slot, 4 channels
+  const int ch = threadIdx.x;                              // folding: one channel (below D)
+  const int row = threadIdx.x / G, l = threadIdx.x % G;    // finishing: an entry, 8 channels
+  const int pos = a.pos0[b];
+  const int len = pos < 0 ? 0 : (a.lens ? min(max(a.lens[b], 0), a.T) : a.T);
   const float* cin = a.carry_in + static_cast<size_t>(b) * 6 * D;
   float* cout = a.carry_out + static_cast<size_t>(b) * 6 * D;
   if (len == 0) {
-    if (job == 0 && cin != cout)
+    if (job == 0 && cin != cout && ch < D)
       for (int i = 0; i < 6; ++i) cout[i * D + ch] = cin[i * D + ch];
     return;
   }
-  const long long end = p0 + len;
-  const long long first = p0 / a.m, last = end / a.m;   // the open blocks before and after
-  const int E = kSlots / a.sg;
-  const T_* za = static_cast<const T_*>(a.z) + static_cast<size_t>(b) * a.T * D;
-  const T_* aa = static_cast<const T_*>(a.a) + static_cast<size_t>(b) * a.T * D;
+  // Positions from here on count from the start of the first block (block `first`):
+  // p0 becomes the tokens already in it.
+  const int first = static_cast<int>(pos) / a.m, p0 = static_cast<int>(pos) - first * a.m;
+  const int end = p0 + len, last = end / a.m;           // tokens, and the open block behind them
+  const T_* za = static_cast<const T_*>(a.z) + static_cast<size_t>(b) * a.T * D + q * 4;
+  const T_* aa = static_cast<const T_*>(a.a) + static_cast<size_t>(b) * a.T * D + q * 4;
 
   // Passes of this CTA: job 0 takes the first block, then the last (the carry
   // goes in and out through one CTA, so carry_out may be carry_in); job k > 0
   // takes E of the blocks strictly between them.
-  const int passes = job == 0 ? (last > first ? 2 : 1) : 1;
+  const int passes = job == 0 && last > 0 ? 2 : 1;
   for (int pass = 0; pass < passes; ++pass) {
-    const long long blk0 = job == 0 ? (pass == 0 ? first : last) : first + 1 + static_cast<long long>(job - 1) * E;
-    const int nblk = job == 0 ? 1 : static_cast<int>(min(static_cast<long long>(E), last - blk0));
+    const int blk0 = job == 0 ? (pass == 0 ? 0 : last) : 1 + (job - 1) * E;
+    const int nblk = job == 0 ? 1 : min(E, last - blk0);
     if (nblk <= 0) return;
-    const int e = slot / a.sg;
-    const bool carried = job == 0 && pass == 0 && p0 % a.m != 0;
-    const long long blk = blk0 + e;
+    const int e = slot / SG;
+    const bool carried = job == 0 && pass == 0 && p0 != 0;
     // fold state of this thread's channel, one per block of the CTA
-    float M[kSlots], Z[kSlots], A[kSlots];
+    float M[E], Z[E], A[E];
     float M1 = -FLT_MAX, Z1 = 0.f, A1 = 0.f;   // the run in progress at the end (job 0)
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) { M[i] = -FLT_MAX; Z[i] = 0.f; A[i] = 0.f; }
-    if (carried) { M[0] = cin[ch]; Z[0] = cin[D + ch]; A[0] = cin[2 * D + ch]; }
-    const long long bend = min((blk0 + 1) * a.m, end);   // job 0: where the block's tokens stop
-    for (int s0 = 0; s0 < a.runs; s0 += a.sg) {
-      const int run = s0 + slot % a.sg;
-      State8 st;
+    for (int i = 0; i < E; ++i) { M[i] = -FLT_MAX; Z[i] = 0.f; A[i] = 0.f; }
+    if (carried && ch < D) { M[0] = cin[ch]; Z[0] = cin[D + ch]; A[0] = cin[2 * D + ch]; }
+    const int bend = min((blk0 + 1) * a.m, end);   // job 0: where the block's tokens stop
+    for (int s0 = 0; s0 < a.runs; s0 += SG) {
+      const int run = s0 + slot % SG;
+      State4 st;
       empty_state(st);
       if (e < nblk && run < a.runs) {
-        const long long lo = blk * a.m + run * kRun;
-        const long long hi = min(lo + kRun, (blk + 1) * a.m);
-        if (carried && lo <= p0 && p0 < hi && p0 > lo) {
-          Vec8<float>::load(cin + 3 * D + l * 8, st.M);
-          Vec8<float>::load(cin + 4 * D + l * 8, st.Z);
-          Vec8<float>::load(cin + 5 * D + l * 8, st.A);
-        }
-        const int t0 = static_cast<int>(max(lo, p0) - p0), t1 = static_cast<int>(min(hi, end) - p0);
-#pragma unroll 4
-        for (int t = t0; t < t1; ++t) {
-          float z8[8], a8[8];
-          Vec8<T_>::load(za + static_cast<size_t>(t) * D + l * 8, z8);
-          Vec8<T_>::load(aa + static_cast<size_t>(t) * D + l * 8, a8);
+        const int lo = (blk0 + e) * a.m + run * kRun;
+        const int hi = min(lo + kRun, (blk0 + e + 1) * a.m);
+        const int t0 = max(lo, p0) - p0, t1 = min(hi, end) - p0;
+        auto start = [&]() {
+          empty_state(st);
+          if (carried && lo < p0 && p0 < hi) {
+            load4(cin + 3 * D + q * 4, st.M);
+            load4(cin + 4 * D + q * 4, st.Z);
+            load4(cin + 5 * D + q * 4, st.A);
+          }
+        };
+        start();
+        if (t1 - t0 == kRun) add_run<T_, D>(st, za + static_cast<size_t>(t0) * D, aa + static_cast<size_t>(t0) * D);
+        else add_tokens<T_, D, false>(st, za, aa, t0, t1);
+        bool fine = true;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) add_token(st.M[c], st.Z[c], st.A[c], z8[c], a8[c]);
+        for (int c = 0; c < 4; ++c) fine = fine && fabsf(st.A[c]) <= FLT_MAX;
+        if (!fine) {
+          start();
+          add_tokens<T_, D, true>(st, za, aa, t0, t1);
         }
       }
-      Vec8<float>::store(&part[slot][0][l * 8], st.M);
-      Vec8<float>::store(&part[slot][1][l * 8], st.Z);
-      Vec8<float>::store(&part[slot][2][l * 8], st.A);
+      store4(&part[slot][0][q * 4], st.M);
+      store4(&part[slot][1][q * 4], st.Z);
+      store4(&part[slot][2][q * 4], st.A);
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < kSlots; ++k) {
-        if (k >= nblk) break;
-        for (int r = 0; r < a.sg && s0 + r < a.runs; ++r) {
-          const int i = k * a.sg + r;
-          const long long lo = (blk0 + k) * a.m + (s0 + r) * kRun;
-          const long long hi = min(lo + kRun, (blk0 + k + 1) * a.m);
+      for (int k = 0; k < E; ++k) {
+        if (k >= nblk || ch >= D) break;
+#pragma unroll
+        for (int r = 0; r < SG; ++r) {
+          if (s0 + r >= a.runs) break;
+          const int i = k * SG + r;
+          const int lo = (blk0 + k) * a.m + (s0 + r) * kRun;
+          const int hi = min(lo + kRun, (blk0 + k + 1) * a.m);
           // job 0: a run that ends behind the tokens is still in progress
           if (job == 0 && hi > bend) {
             if (lo < bend) { M1 = part[i][0][ch]; Z1 = part[i][1][ch]; A1 = part[i][2][ch]; }
@@ -153,47 +264,70 @@ __global__ void __launch_bounds__(kSlots * D / 8) append_kernel(const AppendArgs
       }
       __syncthreads();
     }
-    const bool complete = job != 0 || (pass == 0 && last > first);
+    const bool complete = job != 0 || (pass == 0 && last > 0);
     if (!complete) {
+      if (ch >= D) return;
       cout[ch] = M[0]; cout[D + ch] = Z[0]; cout[2 * D + ch] = A[0];
       cout[3 * D + ch] = M1; cout[4 * D + ch] = Z1; cout[5 * D + ch] = A1;
       return;
     }
 #pragma unroll
-    for (int k = 0; k < kSlots; ++k)
-      if (k < nblk) entry[k][ch] = Z[k] == 0.f ? 0.f : __fdiv_rn(A[k], Z[k]);
-    for (int i = threadIdx.x; i < nblk * (a.R / 2); i += blockDim.x) {
-      const int k = i / (a.R / 2), f = i - k * (a.R / 2);
-      cs[k][f] = cos_sin_at((blk0 + k) * a.m, a.inv_freq[f], a.flags & CSA_ROPE_INVERSE);
-    }
+    for (int k = 0; k < E; ++k)
+      if (ch < D) entry[k][ch] = Z[k] == 0.f ? 0.f : __fdiv_rn(A[k], Z[k]);
     __syncthreads();
-    // slot k finishes entry k
-    float v[8];
-    Vec8<float>::load(&entry[slot][l * 8], v);
-    if (slot >= nblk) {
+    // row k of lanes finishes entry k (whole warps take part: rows behind the last are zeros)
+    if (threadIdx.x < (E * G + 31) / 32 * 32) {
+      float v[8];
+      if (row < nblk) {
+        Vec8<float>::load(&entry[row][l * 8], v);
+      } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = 0.f;
-    }
-    if (a.flags & CSA_NORM) {
-      const float sc = row_rms_scale<D>(v, a.eps);
+        for (int c = 0; c < 8; ++c) v[c] = 0.f;
+      }
+      if (a.flags & CSA_NORM) {
+        const float sc = row_rms_scale<D>(v, a.eps);
+        float w[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = v[c] * sc * (a.weight ? a.weight[l * 8 + c] : 1.f);
-    }
-    LaneRope lr;
-    load_lane_rope<D>(lr, cs[slot < nblk ? slot : 0], a.R, a.flags & CSA_ROPE_HALF, l);
-    rotate8(v, lr, a.R, a.flags & CSA_ROPE_HALF);
-    if (slot < nblk) {
-      const long long s = blk0 + slot;
-      const long long pi = s / a.P;
-      const int hp = min(a.held[b], a.max_pages);
-      const int id = pi < hp ? a.table[static_cast<size_t>(b) * a.max_pages + pi] : -1;
-      if (id >= 0 && id < a.N)
-        Vec8<T_>::store(static_cast<T_*>(a.pool) + (static_cast<size_t>(id) * a.P + s % a.P) * D + l * 8, v);
-      else if (l == 0)
-        atomicCAS(a.status, 0, CSA_ERR_NO_SPACE | (1 << 8));
+        for (int c = 0; c < 8; ++c) w[c] = 1.f;
+        if (a.weight) Vec8<float>::load(a.weight + l * 8, w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] *= sc * w[c];
+      }
+      if (a.R > 0) {
+        LaneRope lr;
+        const long long at = static_cast<long long>(first + blk0 + min(row, nblk - 1)) * a.m;
+        if (a.flags & CSA_ROPE_HALF) {
+          lane_rope_alone<D, true>(lr, at, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
+          rotate8<true>(v, lr, a.R);
+        } else {
+          lane_rope_alone<D, false>(lr, at, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
+          rotate8<false>(v, lr, a.R);
+        }
+      }
+      if (row < nblk) {
+        const int s = first + blk0 + row, pi = s / a.P;
+        const int hp = min(a.held[b], a.max_pages);
+        const int id = pi < hp ? a.table[static_cast<size_t>(b) * a.max_pages + pi] : -1;
+        if (id >= 0 && id < a.N)
+          Vec8<T_>::store(static_cast<T_*>(a.pool) + (static_cast<size_t>(id) * a.P + s % a.P) * D + l * 8, v);
+        else if (l == 0)
+          atomicCAS(a.status, 0, CSA_ERR_NO_SPACE | (1 << 8));
+      }
     }
     __syncthreads();
   }
+}
+
+template <typename T_, int D>
+int launch_append(const AppendArgs& g, int B, int E, cudaStream_t st) {
+  const long long grid = static_cast<long long>(B) * g.ctas_seq;
+  CSA_REQUIRE(grid < (1ll << 31), CSA_ERR_UNSUPPORTED);
+  const unsigned n = static_cast<unsigned>(grid);
+  constexpr int kThreads = kSlots * D / 4;
+  if (E == 1) append_kernel<T_, D, 1><<<n, kThreads, 0, st>>>(g);
+  else if (E == 2) append_kernel<T_, D, 2><<<n, kThreads, 0, st>>>(g);
+  else append_kernel<T_, D, kSlots><<<n, kThreads, 0, st>>>(g);
+  return check_launch();
 }
 
 }  // namespace csa
@@ -205,12 +339,13 @@ extern "C" int hca_paged_append(const void* a, const void* z, int dtype, int B, 
                                 void* pool, int N, int P, const int32_t* table, const int32_t* held, int max_pages,
                                 const float* weight, float eps, const double* inv_freq, int R, int flags,
                                 int32_t* status, csa_stream_t stream) {
-  CSA_REQUIRE(a && z && pos0 && carry_in && carry_out && pool && table && held, CSA_ERR_INVALID_ARG);
+  CSA_REQUIRE((T == 0 || (a && z)) && pos0 && carry_in && carry_out && pool && table && held, CSA_ERR_INVALID_ARG);
   CSA_REQUIRE(B >= 0 && T >= 0 && m >= 1 && N >= 0 && P >= 1 && max_pages >= 1, CSA_ERR_INVALID_ARG);
   CSA_REQUIRE(R >= 0 && R <= D && (R == 0 || inv_freq) && eps >= 0.f, CSA_ERR_INVALID_ARG);
   CSA_REQUIRE((flags & ~(CSA_NORM | CSA_ROPE_INVERSE | CSA_ROPE_HALF)) == 0, CSA_ERR_INVALID_ARG);
   CSA_REQUIRE(dtype == CSA_F32 || dtype == CSA_BF16, CSA_ERR_INVALID_ARG);
   CSA_REQUIRE((D == 64 || D == 128 || D == 256) && R % 16 == 0, CSA_ERR_UNSUPPORTED);
+  CSA_REQUIRE(m <= 65536 && T <= (1 << 30), CSA_ERR_UNSUPPORTED);     // 31-bit token counts
   CSA_REQUIRE(aligned16(a) && aligned16(z) && aligned16(pool) && aligned16(carry_in) && aligned16(carry_out) &&
                   aligned16(weight),
               CSA_ERR_ALIGNMENT);
@@ -225,20 +360,14 @@ extern "C" int hca_paged_append(const void* a, const void* z, int dtype, int B, 
   g.status = status_word(status);
   CSA_REQUIRE(g.status != nullptr, CSA_ERR_CUDA);
   g.runs = (m + kRun - 1) / kRun;
-  // slots per block: a power of two, so that kSlots / sg blocks fit a CTA
-  g.sg = 1;
-  while (g.sg < kSlots && g.sg < g.runs) g.sg *= 2;
-  const int E = kSlots / g.sg;
+  // blocks a CTA sums at once: as many as its slots hold the runs of
+  int E = kSlots;
+  while (E > 1 && kSlots / E < g.runs) E /= 2;
   g.ctas_seq = 1 + (T / m + E - 1) / E;
-  const long long grid = static_cast<long long>(B) * g.ctas_seq;
-  CSA_REQUIRE(grid < (1ll << 31), CSA_ERR_UNSUPPORTED);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-#define AP(TT, DD) append_kernel<TT, DD><<<static_cast<unsigned>(grid), kSlots * DD / 8, 0, st>>>(g)
-  if (dtype == CSA_F32) {
-    if (D == 64) AP(float, 64); else if (D == 128) AP(float, 128); else AP(float, 256);
-  } else {
-    if (D == 64) AP(__nv_bfloat16, 64); else if (D == 128) AP(__nv_bfloat16, 128); else AP(__nv_bfloat16, 256);
-  }
-#undef AP
-  return check_launch();
+  if (dtype == CSA_F32)
+    return D == 64 ? launch_append<float, 64>(g, B, E, st)
+                   : D == 128 ? launch_append<float, 128>(g, B, E, st) : launch_append<float, 256>(g, B, E, st);
+  return D == 64 ? launch_append<__nv_bfloat16, 64>(g, B, E, st)
+                 : D == 128 ? launch_append<__nv_bfloat16, 128>(g, B, E, st) : launch_append<__nv_bfloat16, 256>(g, B, E, st);
 }

@@ -47,7 +47,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <cstdlib>
 #include "common.cuh"
 #include "prefix_attn.cuh"
 
@@ -1037,10 +1036,15 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   CSA_REQUIRE(static_cast<long long>(a.N) * a.P < (1ll << 31), CSA_ERR_UNSUPPORTED);
   CSA_REQUIRE(a.W == 0 || static_cast<long long>(a.B) * a.raw_cap < (1ll << 31), CSA_ERR_UNSUPPORTED);
   a.ppt = 128 / a.H < kPairs ? 128 / a.H : kPairs;
-  // Ranks for the longest sequence that the cache can hold.
+  // Ranks for the longest sequence that the cache can hold, two entry tiles each at
+  // least.  Few heads make few jobs, so up to eight ranks; many heads make a job
+  // a sequence, and four.  (47 x 2 queries of 16 heads, 19 tiles: 23.5 us with 4 ranks, 21.3
+  // with 8; 32 of 64 heads, 34 tiles: 22.5 us with 4, 35.3 with 8, whose clusters do not
+  // all fit at once.)
   const long long tiles = (static_cast<long long>(a.max_pages) * a.P + kTile - 1) / kTile;
-  a.c = tiles < 8 ? 1 : tiles < 16 ? 2 : tiles < 128 ? 4 : 8;
-  if (const char* e = getenv("PA_C")) a.c = atoi(e);
+  const int most_c = a.H > 32 && tiles < 128 ? 4 : 8;
+  a.c = 1;
+  while (a.c < most_c && 4 * a.c <= tiles) a.c *= 2;
   a.log_c = 31 - __builtin_clz(static_cast<unsigned>(a.c));
   // The round-up reciprocal of P for 31-bit numerators: with 2^s the power of two at or
   // above P, ceil(2^(31 + s) / P) fits 32 bits and errs by less than 2^s.

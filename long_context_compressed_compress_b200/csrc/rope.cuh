@@ -34,31 +34,81 @@ __device__ __forceinline__ float row_rms_scale(const float v[8], float eps) {
   return rsqrtf(ss * (1.0f / D) + eps);
 }
 
+// 8 values as loaded.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float v[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <> struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float v[8]) const {
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+    v[4] = __uint_as_float(u.z << 16); v[5] = __uint_as_float(u.z & 0xffff0000u);
+    v[6] = __uint_as_float(u.w << 16); v[7] = __uint_as_float(u.w & 0xffff0000u);
+  }
+};
+
 // The lane's share of the rotation: the cos and sin that its 8 values meet.
 // Interleaved pairs use the first four; split halves one per value.
 struct LaneRope {
   float c[8], s[8];
   bool active, second;   // the lane's values are rotated; they are the pairs' second halves
 };
-// Reads the row's table cs[R / 2] of (cos, sin).
-template <int D>
-__device__ __forceinline__ void load_lane_rope(LaneRope& lr, const float2* cs, int R, bool half, int l) {
+// Lane l of a row at angle pos * inv_freq, the same in the whole warp.  Every lane forms
+// the angles of pairs lane, lane + 32, .. (one for R = 64) and takes those it
+// meets from the others: the 64-bit arithmetic is most of a short call.
+template <int D, bool HALF>
+__device__ __forceinline__ void lane_rope(LaneRope& lr, long long pos, const double* inv_freq, int R, bool inverse,
+                                          int l) {
+  constexpr int N = HALF ? 8 : 4;
+  const int lane = threadIdx.x & 31, pairs = R / 2;
   const int i0 = l * 8 - (D - R);   // the lane's first value within the rotated dims
   lr.active = i0 >= 0 && R > 0;
-  lr.second = half && i0 >= R / 2;
+  lr.second = HALF && i0 >= R / 2;
+  const int p0 = !lr.active ? 0 : HALF ? (lr.second ? i0 - R / 2 : i0) : i0 / 2;
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) {
+    if (32 * k >= pairs) break;
+    float2 mine = make_float2(1.f, 0.f);
+    if (32 * k + lane < pairs) mine = cos_sin_at(pos, inv_freq[32 * k + lane], inverse);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float c = __shfl_sync(0xffffffffu, mine.x, (p0 + i) & 31), s = __shfl_sync(0xffffffffu, mine.y, (p0 + i) & 31);
+      if (k == 0 || ((p0 + i) >> 5) == k) { lr.c[i] = c; lr.s[i] = s; }
+    }
+  }
+}
+// The same where the warp's rows are at different positions: a lane forms what it meets.
+template <int D, bool HALF>
+__device__ __forceinline__ void lane_rope_alone(LaneRope& lr, long long pos, const double* inv_freq, int R, bool inverse,
+                                                int l) {
+  const int i0 = l * 8 - (D - R);
+  lr.active = i0 >= 0 && R > 0;
+  lr.second = HALF && i0 >= R / 2;
   if (!lr.active) return;
-  if (half) {
-    const int p0 = lr.second ? i0 - R / 2 : i0;
+  const int p0 = HALF ? (lr.second ? i0 - R / 2 : i0) : i0 / 2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { const float2 t = cs[p0 + i]; lr.c[i] = t.x; lr.s[i] = t.y; }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { const float2 t = cs[i0 / 2 + i]; lr.c[i] = t.x; lr.s[i] = t.y; }
+  for (int i = 0; i < (HALF ? 8 : 4); ++i) {
+    const float2 t = cos_sin_at(pos, inv_freq[p0 + i], inverse);
+    lr.c[i] = t.x;
+    lr.s[i] = t.y;
   }
 }
 // Rotates the lane's 8 values in place (every lane of the warp takes part).
-__device__ __forceinline__ void rotate8(float v[8], const LaneRope& lr, int R, bool half) {
-  if (half) {
+template <bool HALF>
+__device__ __forceinline__ void rotate8(float v[8], const LaneRope& lr, int R) {
+  if (HALF) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // the partner value sits R / 2 dims away: R / 16 lanes

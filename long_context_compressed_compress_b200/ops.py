@@ -280,83 +280,102 @@ def grouped_out_proj(o, w1, w2, y, out, status=None, stream=None):
         _stream(stream)))
 
 
-def _rows_of(x, heads):
-    """(pointer, batch stride, token stride) of x [B, T, (H,) D] whose heads and
-    values are dense; the batch and token strides are free."""
-    if x is None:
-        return None, 0, 0
-    if not x.is_cuda:
+# The serving calls below run for microseconds, so their checks take each tensor once
+# and the current device and stream by their raw handles (torch's own accessors
+# for these build Python objects).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _home(t):
+    """The device index of a call's tensors: that of ``t``, which has to be the
+    current device (the library launches there)."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensor must be on the GPU")
-    B, T = x.shape[:2]
-    inner = x[0, 0] if B and T else x.new_empty(x.shape[2:])
-    if not inner.is_contiguous():
-        raise ValueError("the values of a token must be contiguous")
-    row = x.shape[-1] * (x.shape[2] if heads else 1)
-    ts = x.stride(1) if T > 1 else row
-    return x.data_ptr(), (x.stride(0) if B > 1 else T * ts), ts
+    if dev != _raw_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_raw_device()}")
+    return dev
 
 
-def _typed(t, dtype, name, shape=None):
-    """The pointer of an optional contiguous tensor of one dtype (and shape)."""
+def _arg(t, name, dtype, shape, dev):
+    """The pointer of a contiguous tensor of that dtype, shape (None: any) and device;
+    None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return _ptr(t)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _same(*ts):
-    """All (non-None) tensors on one device, the current one."""
-    dev = {t.device for t in ts if t is not None}
-    if len(dev) > 1:
-        raise ValueError(f"tensors are on several devices: {sorted(map(str, dev))}")
-    for d in dev:
-        if d.type == "cuda" and d.index != torch.cuda.current_device():
-            raise ValueError(f"tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
+def _on(stream, dev):
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _rope_flags(norm, interleaved, inverse):
-    return (NORM if norm else 0) | (0 if interleaved else ROPE_HALF) | (ROPE_INVERSE if inverse else 0)
+def _code(dtype):
+    if dtype is torch.bfloat16:
+        return CSA_BF16
+    if dtype is torch.float32:
+        return CSA_F32
+    raise ValueError(f"unsupported dtype {dtype}")
+
+
+def _rope_args(inv_freq, norm, interleaved, inverse, dev):
+    """(pointer of the frequencies, rotated dims, flags)"""
+    flags = (NORM if norm else 0) | (0 if interleaved else ROPE_HALF) | (ROPE_INVERSE if inverse else 0)
+    if inv_freq is None:
+        return None, 0, flags
+    return _arg(inv_freq, "inv_freq", torch.float64, None, dev), 2 * inv_freq.numel(), flags
 
 
 def qk_norm_rope(q, kv, q_out, kv_out, q_pos0, inv_freq=None, q_weight=None, kv_weight=None, eps=1e-6, norm=True,
                  interleaved=True, inverse=False, pos_step=1, lens=None, stream=None):
     """RMS norm per head and position rotation of the queries q [B, T, H, D] and
     the shared key kv [B, T, D] in one pass (either pair may be None).  Token t
-    is at j = q_pos0[b] + t and is rotated by j * pos_step * inv_freq; its key
-    goes to slot j % cap of kv_out [B, cap, D].  q and kv may be views with free
-    batch and token strides (slices of one projection's output)."""
-    _same(q, kv, q_out, kv_out, q_pos0, inv_freq, q_weight, kv_weight, lens)
+    is at j = q_pos0[b] + t and is rotated by j * pos_step * inv_freq (float64
+    [R / 2]; the last R dims); its key goes to slot j % cap of kv_out [B, cap, D].
+    q and kv may be views with free batch and token strides (slices of one
+    projection's output).  Tokens from lens[b] on are left alone."""
     if (q is None) != (q_out is None) or (kv is None) != (kv_out is None) or (q is None and kv is None):
         raise ValueError("q with q_out, kv with kv_out, at least one pair")
     x = q if q is not None else kv
-    B, T, D = x.shape[0], x.shape[1], x.shape[-1]
-    H = q.shape[2] if q is not None else 0
-    cap = 0
-    if q is not None and (q_out.dtype != q.dtype or q_out.shape != q.shape):
-        raise ValueError("q_out must have q's shape and dtype")
-    if kv is not None:
-        cap = kv_out.shape[1]
-        if kv.dtype != x.dtype or kv_out.dtype != x.dtype or kv.shape != (B, T, D) or kv_out.shape != (B, cap, D):
-            raise ValueError("kv must be [B, T, D] and kv_out [B, cap, D], of q's dtype")
-    if T == 0 or B == 0:
+    dev, dt = _home(x), x.dtype
+    if not x.numel():
         return
-    qp, qb, qt = _rows_of(q, True)
-    kp, kb, kt = _rows_of(kv, False)
-    R = 0 if inv_freq is None else 2 * inv_freq.numel()
+    B, T, D = x.shape[0], x.shape[1], x.shape[-1]
+    H = cap = qb = qt = kb = kt = 0
+    qp = qop = kp = kop = None
+    if q is not None:
+        _, _, H, _ = q.shape
+        qb, qt, sh, sd = q.stride()
+        if (sd != 1 and D > 1) or (sh != D and H > 1):
+            raise ValueError("the heads of a token of q must be contiguous")
+        qt = qt if T > 1 else H * D
+        qb = qb if B > 1 else T * qt
+        qp, qop = q.data_ptr(), _arg(q_out, "q_out", dt, q.shape, dev)
+    if kv is not None:
+        if kv.shape != (B, T, D) or kv.dtype is not dt or kv.get_device() != dev:
+            raise ValueError("kv must be [B, T, D], of q's dtype and device")
+        kb, kt, sd = kv.stride()
+        if sd != 1 and D > 1:
+            raise ValueError("the values of a token of kv must be contiguous")
+        kt = kt if T > 1 else D
+        kb = kb if B > 1 else T * kt
+        cap = kv_out.shape[1]
+        kp, kop = kv.data_ptr(), _arg(kv_out, "kv_out", dt, (B, cap, D), dev)
+    fp, R, flags = _rope_args(inv_freq, norm, interleaved, inverse, dev)
     _check("qk_norm_rope", lib.qk_norm_rope(
-        qp, qb, qt, kp, kb, kt, _dt(x), B, T, H, D, _typed(q_pos0, torch.int32, "q_pos0", (B,)),
-        _typed(lens, torch.int32, "lens", (B,)), pos_step, _typed(inv_freq, torch.float64, "inv_freq"), R,
-        _typed(q_weight, torch.float32, "q_weight", (D,)), _typed(kv_weight, torch.float32, "kv_weight", (D,)), eps,
-        _rope_flags(norm, interleaved, inverse), _ptr(q_out), _ptr(kv_out), cap, _stream(stream)))
-
-
-def _cache_args(table, held, refcount=None):
-    R, maxp = table.shape
-    return (_typed(table, torch.int32, "table"), _typed(held, torch.int32, "held", (R,)), R, maxp,
-            _typed(refcount, torch.int32, "refcount"))
+        qp, qb, qt, kp, kb, kt, _code(dt), B, T, H, D, _arg(q_pos0, "q_pos0", torch.int32, (B,), dev),
+        _arg(lens, "lens", torch.int32, (B,), dev), pos_step, fp, R,
+        _arg(q_weight, "q_weight", torch.float32, (D,), dev), _arg(kv_weight, "kv_weight", torch.float32, (D,), dev),
+        eps, flags, qop, kop, cap, _on(stream, dev)))
 
 
 def hca_paged_append(a, z, pos0, carry, pool, table, held, m, carry_out=None, lens=None, norm=False, weight=None,
@@ -364,107 +383,108 @@ def hca_paged_append(a, z, pos0, carry, pool, table, held, m, carry_out=None, le
     """Pool new tokens a, z [B, T, D] (gates z) into paged entries pool [N, P, D];
     carry [B, 2, 3, D] float32 holds the open blocks and is updated in place, or
     into carry_out.  Entries are optionally normalised and rotated at m * index."""
-    carry_out = carry if carry_out is None else carry_out
-    _same(a, z, pos0, carry, carry_out, pool, table, held, lens, weight, inv_freq, status)
+    dev, dt = _home(a), a.dtype
     B, T, D = a.shape
-    if z.shape != a.shape or z.dtype != a.dtype or pool.dtype != a.dtype or pool.dim() != 3 or pool.shape[2] != D:
-        raise ValueError("a and z must be [B, T, D], pool [N, P, D], of one dtype")
-    if table.shape[0] != B:
-        raise ValueError("table must have one row per sequence")
-    tp, hp, _, maxp, _ = _cache_args(table, held)
+    N, P_, _ = pool.shape
+    maxp = table.shape[1]
+    state = (B, 2, 3, D)
+    cp = _arg(carry, "carry", torch.float32, state, dev)
+    fp, R, flags = _rope_args(inv_freq, norm, interleaved, inverse, dev)
     _check("hca_paged_append", lib.hca_paged_append(
-        _ptr(a), _ptr(z), _dt(a), B, T, D, m, _typed(pos0, torch.int32, "pos0", (B,)),
-        _typed(lens, torch.int32, "lens", (B,)), _typed(carry, torch.float32, "carry", (B, 2, 3, D)),
-        _typed(carry_out, torch.float32, "carry_out", (B, 2, 3, D)), _ptr(pool), pool.shape[0], pool.shape[1], tp, hp,
-        maxp, _typed(weight, torch.float32, "weight", (D,)), eps, _typed(inv_freq, torch.float64, "inv_freq"),
-        0 if inv_freq is None else 2 * inv_freq.numel(), _rope_flags(norm, interleaved, inverse),
-        _typed(status, torch.int32, "status"), _stream(stream)))
+        _arg(a, "a", dt, None, dev), _arg(z, "z", dt, (B, T, D), dev), _code(dt), B, T, D, m,
+        _arg(pos0, "pos0", torch.int32, (B,), dev), _arg(lens, "lens", torch.int32, (B,), dev), cp,
+        cp if carry_out is None else _arg(carry_out, "carry_out", torch.float32, state, dev),
+        _arg(pool, "pool", dt, (N, P_, D), dev), N, P_, _arg(table, "table", torch.int32, (B, maxp), dev),
+        _arg(held, "held", torch.int32, (B,), dev), maxp, _arg(weight, "weight", torch.float32, (D,), dev), eps, fp, R,
+        flags, _arg(status, "status", torch.int32, None, dev), _on(stream, dev)))
 
 
-def hca_prefix_attn_fwd(q, pool, table, held, groups, kv_raw, sink, tau, W, q_pos0, out, m, lse=None, raw_cap=None,
-                        status=None, stream=None):
+def hca_prefix_attn_fwd(q, pool, table, held, groups, kv_raw, sink, tau, W, q_pos0, out, m, lse=None, status=None,
+                        stream=None):
     """HCA attention of q [B, T, H, D] over paged entries pool [N, P, D], the raw
     window kv_raw [B, raw_cap, D] and the sink; ``groups`` (paged.PrefixGroups)
     names the sequences that share their first pages."""
+    dev, dt = _home(q), q.dtype
+    if not q.numel():
+        return
     B, T, H, D = q.shape
-    _same(q, pool, table, held, groups.off, kv_raw, sink, q_pos0, out, lse, status)
-    if pool.dtype != q.dtype or pool.dim() != 3 or pool.shape[2] != D or out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("pool must be [N, P, D] and out [B, T, H, D], of q's dtype")
-    if table.shape[0] != B or groups.B != B:
-        raise ValueError("table and groups must be those of the batch")
-    if W and (kv_raw is None or kv_raw.dtype != q.dtype or kv_raw.dim() != 3 or kv_raw.shape[0] != B
-              or kv_raw.shape[2] != D or (raw_cap is not None and raw_cap > kv_raw.shape[1])):
-        raise ValueError("kv_raw must be [B, raw_cap, D] of q's dtype")
-    raw_cap = (kv_raw.shape[1] if kv_raw is not None else 1) if raw_cap is None else raw_cap
-    if W and raw_cap != kv_raw.shape[1] and B > 1:
-        raise ValueError("raw_cap must be kv_raw's")
-    tp, hp, _, maxp, _ = _cache_args(table, held)
+    N, P_, _ = pool.shape
+    maxp = table.shape[1]
+    if groups.B != B or groups.dev != dev:
+        raise ValueError("groups must be those of the batch, on its device")
+    raw_cap = 1 if kv_raw is None else kv_raw.shape[1]
     _check("hca_prefix_attn_fwd", lib.hca_prefix_attn_fwd(
-        _ptr(q), _ptr(pool), pool.shape[0], pool.shape[1], tp, hp, maxp, _ptr(groups.off), _ptr(groups.seq),
-        _ptr(groups.shared), groups.G, groups.n_seq, _ptr(kv_raw), _typed(sink, torch.float32, "sink", (H,)), tau, W,
-        B, T, H, D, m, raw_cap, _typed(q_pos0, torch.int32, "q_pos0", (B,)), _ptr(out),
-        _typed(lse, torch.float32, "lse", (B, T, H)), _dt(q), _typed(status, torch.int32, "status"),
-        _stream(stream)))
+        _arg(q, "q", dt, None, dev), _arg(pool, "pool", dt, (N, P_, D), dev), N, P_,
+        _arg(table, "table", torch.int32, (B, maxp), dev), _arg(held, "held", torch.int32, (B,), dev), maxp,
+        groups.off_ptr, groups.seq_ptr, groups.shared_ptr, groups.G, groups.n_seq,
+        _arg(kv_raw, "kv_raw", dt, (B, raw_cap, D), dev), _arg(sink, "sink", torch.float32, (H,), dev), tau, W, B, T, H,
+        D, m, raw_cap, _arg(q_pos0, "q_pos0", torch.int32, (B,), dev), _arg(out, "out", dt, (B, T, H, D), dev),
+        _arg(lse, "lse", torch.float32, (B, T, H), dev), _code(dt), _arg(status, "status", torch.int32, None, dev),
+        _on(stream, dev)))
 
 
 def kv_pages_workspace_size(N, n):
+    """Bytes of workspace for a cache of N pages and lists of n rows (0 for compact)."""
     return int(lib.kv_pages_workspace_size(N, n))
 
 
-def _ws(workspace):
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+def _cache_args(table, held, refcount, dev):
+    R, maxp = table.shape
+    return (_arg(table, "table", torch.int32, None, dev), _arg(held, "held", torch.int32, (R,), dev), R, maxp,
+            _arg(refcount, "refcount", torch.int32, None, dev), refcount.numel())
 
 
-def _layers(pool, refcount):
+def _ws(workspace, dev):
+    return _arg(workspace, "workspace", torch.int32, None, dev), workspace.numel() * 4
+
+
+def _layers(pool, N, dev):
     """(pointer, L, bytes of one layer's page) of pool [L, N, P, D]."""
-    if pool.dim() != 4 or pool.shape[1] != refcount.numel():
+    L, n, P_, D = pool.shape
+    if n != N:
         raise ValueError("pool must be [L, N, P, D] with refcount [N]")
-    return _ptr(pool), pool.shape[0], pool.shape[2] * pool.shape[3] * pool.element_size()
+    return _arg(pool, "pool", pool.dtype, None, dev), L, P_ * D * pool.element_size()
 
 
 def kv_pages_reserve(rows, n_entries, P, table, held, refcount, workspace, status=None, stream=None):
     """Grow the listed rows to hold n_entries entries each (pages of P)."""
-    _same(rows, n_entries, table, held, refcount, workspace, status)
-    tp, hp, R, maxp, rp = _cache_args(table, held, refcount)
-    n = rows.numel()
+    dev, n = _home(table), rows.numel()
+    tp, hp, R, maxp, rp, N = _cache_args(table, held, refcount, dev)
     _check("kv_pages_reserve", lib.kv_pages_reserve(
-        _typed(rows, torch.int32, "rows", (n,)), _typed(n_entries, torch.int32, "n_entries", (n,)), n, P, tp, hp, R,
-        maxp, rp, refcount.numel(), *_ws(workspace), _typed(status, torch.int32, "status"), _stream(stream)))
+        _arg(rows, "rows", torch.int32, (n,), dev), _arg(n_entries, "n_entries", torch.int32, (n,), dev), n, P, tp, hp,
+        R, maxp, rp, N, *_ws(workspace, dev), _arg(status, "status", torch.int32, None, dev), _on(stream, dev)))
 
 
 def kv_pages_fork(src, dst, n_entries, pool, table, held, refcount, workspace, status=None, stream=None):
     """Make each empty row dst[i] share the first n_entries[i] entries of src[i];
     pool [L, N, P, D] (a partial last page is copied in every layer)."""
-    _same(src, dst, n_entries, pool, table, held, refcount, workspace, status)
-    tp, hp, R, maxp, rp = _cache_args(table, held, refcount)
-    n = dst.numel()
-    pp, L, page = _layers(pool, refcount)
+    dev, n = _home(table), dst.numel()
+    tp, hp, R, maxp, rp, N = _cache_args(table, held, refcount, dev)
+    pp, L, page = _layers(pool, N, dev)
     _check("kv_pages_fork", lib.kv_pages_fork(
-        _typed(src, torch.int32, "src", (n,)), _typed(dst, torch.int32, "dst", (n,)),
-        _typed(n_entries, torch.int32, "n_entries", (n,)), n, pool.shape[2], tp, hp, R, maxp, rp, refcount.numel(), pp,
-        L, page, *_ws(workspace), _typed(status, torch.int32, "status"), _stream(stream)))
+        _arg(src, "src", torch.int32, (n,), dev), _arg(dst, "dst", torch.int32, (n,), dev),
+        _arg(n_entries, "n_entries", torch.int32, (n,), dev), n, pool.shape[2], tp, hp, R, maxp, rp, N, pp, L, page,
+        *_ws(workspace, dev), _arg(status, "status", torch.int32, None, dev), _on(stream, dev)))
 
 
 def kv_pages_free(rows, table, held, refcount, status=None, stream=None):
     """Give up the pages of the listed rows."""
-    _same(rows, table, held, refcount, status)
-    tp, hp, R, maxp, rp = _cache_args(table, held, refcount)
-    n = rows.numel()
+    dev, n = _home(table), rows.numel()
+    tp, hp, R, maxp, rp, N = _cache_args(table, held, refcount, dev)
     _check("kv_pages_free", lib.kv_pages_free(
-        _typed(rows, torch.int32, "rows", (n,)), n, tp, hp, R, maxp, rp, refcount.numel(),
-        _typed(status, torch.int32, "status"), _stream(stream)))
+        _arg(rows, "rows", torch.int32, (n,), dev), n, tp, hp, R, maxp, rp, N,
+        _arg(status, "status", torch.int32, None, dev), _on(stream, dev)))
 
 
 def kv_pages_compact(pool, table, held, refcount, n_live, workspace, table_out=None, refcount_out=None, stream=None):
     """Move the pages in use to the ids [0, n_live) (pool [L, N, P, D] in place);
     the new metadata goes to table_out / refcount_out (default: in place) and
     the number of pages in use to n_live int32 [1]."""
-    table_out = table if table_out is None else table_out
-    refcount_out = refcount if refcount_out is None else refcount_out
-    _same(pool, table, held, refcount, n_live, workspace, table_out, refcount_out)
-    tp, hp, R, maxp, rp = _cache_args(table, held, refcount)
-    pp, L, page = _layers(pool, refcount)
+    dev = _home(table)
+    tp, hp, R, maxp, rp, N = _cache_args(table, held, refcount, dev)
+    pp, L, page = _layers(pool, N, dev)
     _check("kv_pages_compact", lib.kv_pages_compact(
-        tp, hp, R, maxp, rp, refcount.numel(), pp, L, page, _typed(table_out, torch.int32, "table_out", table.shape),
-        _typed(refcount_out, torch.int32, "refcount_out", refcount.shape),
-        _typed(n_live, torch.int32, "n_live", (1,)), *_ws(workspace), _stream(stream)))
+        tp, hp, R, maxp, rp, N, pp, L, page,
+        tp if table_out is None else _arg(table_out, "table_out", torch.int32, (R, maxp), dev),
+        rp if refcount_out is None else _arg(refcount_out, "refcount_out", torch.int32, (N,), dev),
+        _arg(n_live, "n_live", torch.int32, (1,), dev), *_ws(workspace, dev), _on(stream, dev)))

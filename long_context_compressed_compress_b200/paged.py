@@ -32,6 +32,9 @@ class PrefixGroups:
         self.B, self.G, self.n_seq = int(B), len(shared), len(seq)
         self.off, self.seq, self.shared = (torch.tensor(v or [0], dtype=torch.int32).to(device)
                                            for v in (off, seq, shared))
+        # what a call passes on (this object owns the tensors behind the pointers)
+        self.dev = self.off.get_device()
+        self.off_ptr, self.seq_ptr, self.shared_ptr = (t.data_ptr() for t in (self.off, self.seq, self.shared))
 
     @staticmethod
     def singles(B, device="cuda"):
