@@ -13,14 +13,22 @@ CSA prefill (cf-1.com/news/5231315 §3.1, §3.3, §3.4):
 HCA prefill (§3.2, §3.3):
     hca_compress(a, z)            -> kv_c  [B, S, D]
     hca_dense_attn_fwd            -> out
+HCA decode over paged entries that sequences may share (§4.4):
+    qk_norm_rope / csa_ring_append  this step's raw KV -> window ring
+    hca_paged_append              -> the entry of a completed block, in its page
+    hca_prefix_attn_fwd           -> out
+With a NormRope the queries, raw keys and entries are normalised and rotated by
+position before the attention, and its output is rotated back.
 """
 from __future__ import annotations
 
 import os
+from dataclasses import dataclass
+from typing import Optional
 
 import torch
 
-from . import ops
+from . import ops, paged
 
 _DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 
@@ -49,11 +57,53 @@ def raise_on_status(status):
         raise ops.CsaError("device check", v & 0xFF)
 
 
+@dataclass
+class NormRope:
+    """Norm and position rotation of a layer's queries, raw keys and entries.
+
+    Queries and keys are RMS-normalised per head (weights float32 [D] or None for
+    ones) and their last 2 * len(inv_freq) dims rotated by position * inv_freq
+    (float64, radians per token); an entry is at its block's first position, m * s.
+    Since keys are values too, ``derotate`` turns the attention's output back by
+    the query's position, so that it depends on relative positions only."""
+
+    inv_freq: Optional[torch.Tensor] = None
+    q_weight: Optional[torch.Tensor] = None
+    kv_weight: Optional[torch.Tensor] = None
+    entry_weight: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    norm: bool = True
+    interleaved: bool = True
+    derotate: bool = True
+
+    def _kw(self):
+        return dict(inv_freq=self.inv_freq, eps=self.eps, norm=self.norm, interleaved=self.interleaved)
+
+    def queries(self, q, kv, q_out, kv_out, q_pos0, lens=None):
+        ops.qk_norm_rope(q, kv, q_out, kv_out, q_pos0, q_weight=self.q_weight, kv_weight=self.kv_weight, lens=lens,
+                         **self._kw())
+
+    def entries(self, kv_c, m, zeros):
+        """Entries [B, S, D] of a prefill, in place."""
+        if kv_c.numel():
+            ops.qk_norm_rope(None, kv_c, None, kv_c, zeros, kv_weight=self.entry_weight, pos_step=m, **self._kw())
+
+    def back(self, out, q_pos0):
+        """The attention's output, in place."""
+        if self.derotate and self.inv_freq is not None:
+            ops.qk_norm_rope(out, None, out, None, q_pos0, inv_freq=self.inv_freq, norm=False, inverse=True,
+                             interleaved=self.interleaved)
+
+    @property
+    def launches(self):
+        return 3 if self.derotate and self.inv_freq is not None else 2
+
+
 class CsaPrefill:
     """Buffers + call sequence of one CSA prefill layer.  ``chunk`` bounds the
     query rows scored at once (the score buffer is [B, chunk, S])."""
 
-    def __init__(self, cfg, device="cuda", chunk=None, gscale=1.0, fused=None, check=None):
+    def __init__(self, cfg, device="cuda", chunk=None, gscale=1.0, fused=None, check=None, norm_rope=None):
         self.cfg = cfg
         c = cfg
         dt = _DT[c.dtype]
@@ -85,6 +135,11 @@ class CsaPrefill:
         self.check = _check_mode(check)
         self.status = torch.zeros((1,), dtype=torch.int32, device=device) if self.check else None
         self.launches += ((c.T + self.chunk - 1) // self.chunk) if self.check else 0
+        self.norm_rope = norm_rope
+        if norm_rope is not None:
+            self.q_n = torch.empty_like(self.out)
+            self.raw_n = torch.empty((c.B, c.T, c.D), dtype=dt, device=device)
+            self.launches += norm_rope.launches
 
     def run(self, x, keep_idx=None, timer=None):
         """x: dict of device tensors (input generator order).  If ``keep_idx`` is a
@@ -99,6 +154,12 @@ class CsaPrefill:
                              gscale=self.g, out_dtype=x["a_I"].dtype)
         with t("nvfp4_quantize"):
             ops.nvfp4_quantize(x["q_I"], self.q_fp4, self.q_sf, self.g)
+        q, raw = x["q"], x["kv_raw"]
+        if self.norm_rope is not None:
+            with t("qk_norm_rope"):
+                self.norm_rope.entries(self.kv_c, c.m, self.q_pos0)
+                self.norm_rope.queries(q, raw, self.q_n, self.raw_n, self.q_pos0)
+            q, raw = self.q_n, self.raw_n
         for r0 in range(0, c.T, self.chunk):
             tc = min(self.chunk, c.T - r0)
             ix = self.idx.view(-1)[: c.B * tc * c.k].view(c.B, tc, c.k)
@@ -116,10 +177,12 @@ class CsaPrefill:
             if self.check:
                 ops.validate_indices(ix, c.S, c.m, self.q_pos0, self.status, row0=r0)
             with t("sparse_attn_fwd"):
-                ops.sparse_attn_fwd(x["q"], self.kv_c, ix, x["kv_raw"], x["sink"], c.tau, c.W, self.q_pos0,
+                ops.sparse_attn_fwd(q, self.kv_c, ix, raw, x["sink"], c.tau, c.W, self.q_pos0,
                                     self.out, self.lse, row0=r0, T_chunk=tc)
             if keep_idx is not None:
                 keep_idx[:, r0:r0 + tc].copy_(ix)
+        if self.norm_rope is not None:
+            self.norm_rope.back(self.out, self.q_pos0)
         if self.check:
             raise_on_status(self.status)
         return self.out
@@ -128,7 +191,7 @@ class CsaPrefill:
 class HcaPrefill:
     """Buffers + call sequence of one HCA prefill layer."""
 
-    def __init__(self, cfg, device="cuda"):
+    def __init__(self, cfg, device="cuda", norm_rope=None):
         self.cfg = cfg
         c = cfg
         dt = _DT[c.dtype]
@@ -137,15 +200,28 @@ class HcaPrefill:
         self.lse = None
         self.q_pos0 = torch.zeros((c.B,), dtype=torch.int32, device=device)
         self.launches = 2
+        self.norm_rope = norm_rope
+        if norm_rope is not None:
+            self.q_n = torch.empty_like(self.out)
+            self.raw_n = torch.empty((c.B, c.T, c.D), dtype=dt, device=device)
+            self.launches += norm_rope.launches
 
     def run(self, x, timer=None):
         c = self.cfg
         t = timer or _no_timer
         with t("hca_compress"):
             ops.hca_compress(x["a"], x["z"], c.m, self.kv_c)
+        q, raw = x["q"], x["kv_raw"]
+        if self.norm_rope is not None:
+            with t("qk_norm_rope"):
+                self.norm_rope.entries(self.kv_c, c.m, self.q_pos0)
+                self.norm_rope.queries(q, raw, self.q_n, self.raw_n, self.q_pos0)
+            q, raw = self.q_n, self.raw_n
         with t("hca_dense_attn_fwd"):
-            ops.hca_dense_attn_fwd(x["q"], self.kv_c, x["kv_raw"], x["sink"], c.tau, c.W, self.q_pos0, self.out,
+            ops.hca_dense_attn_fwd(q, self.kv_c, raw, x["sink"], c.tau, c.W, self.q_pos0, self.out,
                                    c.m, lse=self.lse)
+        if self.norm_rope is not None:
+            self.norm_rope.back(self.out, self.q_pos0)
         return self.out
 
 
@@ -286,6 +362,122 @@ class CsaDecode:
                 self.step(x)
         torch.cuda.current_stream().wait_stream(s)
         self.pos.copy_(p0)
+        self.graph = g
+        return g
+
+    def replay(self):
+        self.graph.replay()
+        return self.out
+
+
+class HcaDecode:
+    """Buffers + call sequence of one HCA decode step: one new token for each of
+    the cache's R rows (cf-1.com/news/5231315 §3.2, §3.3), over entries in pages
+    that rows may share (§4.4).
+
+    ``cache`` (paged.PagedEntries) holds the entries of layer ``layer``; rows need
+    pages for the entries they are about to complete (``cache.reserve``).  The rest
+    of a row's state is here: pos int32 [R] (tokens seen), the raw window ring
+    [R, W, D] and the compressor's carry [R, 2, 3, D].  ``groups``
+    (paged.PrefixGroups, default: every row by itself) names the rows that share
+    their first pages and, by leaving rows out, those that are idle: their
+    outputs are left as they were (their state advances all the same).
+
+        qk_norm_rope or csa_ring_append   token's raw KV -> ring slot pos % W
+        hca_paged_append                  block pooling; a completed entry -> its page
+        hca_prefix_attn_fwd               out [R, 1, H, D] (window + sink fused)
+        csa_pos_advance                   pos += 1 on the device
+
+    Every launch reads positions and pages on the device, so the step can be captured
+    in a CUDA graph (``capture``) and replayed; a capture holds its ``groups``."""
+
+    def __init__(self, cfg, cache, sink=None, layer=0, groups=None, norm_rope=None, with_lse=False, device="cuda"):
+        self.cfg, self.cache, self.layer, self.sink, self.norm_rope = cfg, cache, layer, sink, norm_rope
+        R, D = cache.R, cfg.D
+        dt = _DT[cfg.dtype]
+        self.pos = torch.zeros((R,), dtype=torch.int32, device=device)
+        self.ring = torch.zeros((R, cfg.W, D), dtype=dt, device=device)
+        self.carry = torch.zeros((R, 2, 3, D), dtype=torch.float32, device=device)
+        self.out = torch.zeros((R, 1, cfg.H, D), dtype=dt, device=device)
+        self.lse = torch.zeros((R, 1, cfg.H), dtype=torch.float32, device=device) if with_lse else None
+        self.q_n = torch.empty_like(self.out) if norm_rope is not None else None
+        self.groups = groups or paged.PrefixGroups.singles(R, device=device)
+        self.launches = 4 + (norm_rope.launches - 2 if norm_rope is not None else 0)
+        self.graph = None
+
+    def _append(self, a, z, lens=None):
+        nr = self.norm_rope
+        c = self.cache
+        kw = {} if nr is None else dict(norm=nr.norm, weight=nr.entry_weight, eps=nr.eps, inv_freq=nr.inv_freq,
+                                        interleaved=nr.interleaved)
+        ops.hca_paged_append(a, z, self.pos, self.carry, c.pool[self.layer], c.table, c.held, self.cfg.m, lens=lens,
+                             status=c.status, **kw)
+
+    def load(self, x, lens=None):
+        """Take prompts a, z, kv_raw [R, T, D] (row r's first lens[r] tokens; lens
+        int32 [R] on the device, T for all by default) behind what the rows hold."""
+        R, T, _ = x["a"].shape
+        nr = self.norm_rope or NormRope(norm=False)
+        nr.queries(None, x["kv_raw"], None, self.ring, self.pos, lens)
+        self._append(x["a"], x["z"], lens)
+        self.pos += T if lens is None else lens.clamp(0, T)
+
+    def step(self, x, timer=None):
+        """x: this step's a, z, kv_raw [R, D] and q [R, H, D] on the device.
+        Returns out [R, 1, H, D]."""
+        c = self.cfg
+        t = timer or _no_timer
+        R = self.cache.R
+        q, raw = x["q"].view(R, 1, c.H, c.D), x["kv_raw"].view(R, 1, c.D)
+        if self.norm_rope is not None:
+            with t("qk_norm_rope"):
+                self.norm_rope.queries(q, raw, self.q_n, self.ring, self.pos)
+            q = self.q_n
+        else:
+            with t("csa_ring_append"):
+                ops.csa_ring_append(x["kv_raw"], self.ring, self.pos)
+        with t("hca_paged_append"):
+            self._append(x["a"].view(R, 1, c.D), x["z"].view(R, 1, c.D))
+        with t("hca_prefix_attn_fwd"):
+            ops.hca_prefix_attn_fwd(q, self.cache.pool[self.layer], self.cache.table, self.cache.held, self.groups,
+                                    self.ring, self.sink, c.tau, c.W, self.pos, self.out, c.m, lse=self.lse,
+                                    status=self.cache.status)
+        if self.norm_rope is not None:
+            self.norm_rope.back(self.out, self.pos)
+        with t("csa_pos_advance"):
+            ops.csa_pos_advance(self.pos, 1)
+        return self.out
+
+    def entries(self):
+        """Complete entries of every row, int32 [R] (what a fork shares)."""
+        return torch.div(self.pos, self.cfg.m, rounding_mode="floor").to(torch.int32)
+
+    def copy_state(self, src, dst):
+        """Rows dst take the window, carry and position of rows src (int64 index
+        tensors); the entries are the cache's to fork."""
+        for t in (self.pos, self.ring, self.carry):
+            t[dst] = t[src]
+
+    def fork(self, src, dst):
+        """Empty rows dst (lists or int32 tensors) become copies of rows src: whole
+        pages shared, the last partial page and the rest of the state copied.  A
+        cache of several layers is forked once, the other layers' states copied by
+        their own ``copy_state``."""
+        src, dst = self.cache._list(src), self.cache._list(dst)
+        self.cache.fork(src, dst, self.entries()[src.long()])
+        self.copy_state(src.long(), dst.long())
+
+    def capture(self, x):
+        """Record one step on static input buffers ``x`` into a CUDA graph (run
+        ``step`` once before: first-call set-up must not happen inside the
+        capture).  Capturing does not advance the rows."""
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s):
+            with torch.cuda.graph(g, stream=s):
+                self.step(x)
+        torch.cuda.current_stream().wait_stream(s)
         self.graph = g
         return g
 
