@@ -309,7 +309,7 @@ __device__ __forceinline__ int group_start(const Args& a, int g) {
 
 // Warp 0: the job's group and tile of pairs (jobs are numbered group by group); false
 // when there is no such job.
-__device__ bool find_job(const Args& a, int job, Smem& sm, int* start, int* count) {
+__device__ bool find_job(const Args& a, int job, Smem* sm, int* start, int* count) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int g0 = 0; g0 < a.G; g0 += 32) {
@@ -324,9 +324,9 @@ __device__ bool find_job(const Args& a, int job, Smem& sm, int* start, int* coun
     const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > job);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      if (lane == src) {
-        sm.group = g;
-        sm.tile = job - (before + incl - jobs);
+      if (sm != nullptr && lane == src) {
+        sm->group = g;
+        sm->tile = job - (before + incl - jobs);
       }
       *start = __shfl_sync(0xffffffffu, o0, src);
       *count = __shfl_sync(0xffffffffu, n, src);
@@ -426,6 +426,24 @@ __device__ __noinline__ void row_exact(const Args& a, const Pair& pr, int h, flo
   if (a.lse && lane == 0) a.lse[row] = lse;
 }
 
+// The factor of O and the lse of a row with stabiliser M and sum L (log2 domain).
+__device__ __forceinline__ void finish_row(float M, float L, float sink_l2, float* sc, float* lse) {
+  *sc = 0.f;
+  *lse = -INFINITY;
+  if (L != 0.f) {
+    const float X = fmaxf(M, sink_l2), fm = ex2(M - X);
+    *sc = __fdiv_rn(fm, fmaf(L, fm, ex2(sink_l2 - X)));
+    *lse = (M + log2f(L)) * 0.6931471805599453f;
+  }
+}
+
+// Entry `key` of sequence b as a row of the pool, or -1.
+__device__ __forceinline__ int entry_row(const Args& a, int b, int key) {
+  const int pg = a.P > 1 ? static_cast<int>(__umulhi(key, a.p_mul) >> a.p_shift) : key;
+  const int id = a.table[static_cast<size_t>(b) * a.max_pages + pg];
+  return id >= 0 && id < a.N ? id * a.P + (key - pg * a.P) : -1;
+}
+
 // How many of this rank's entry tiles lie in [i0, ceil(n / 128)).
 __device__ __forceinline__ int tiles_of(int i0, int n, int log_c) {
   const int end = static_cast<int>((static_cast<uint32_t>(n) + kTile - 1) / kTile);
@@ -444,11 +462,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
   const int rank = static_cast<int>(cluster_rank());
-  const int job = blockIdx.x / a.c;
+  const int job = blockIdx.x >> a.log_c;
 
-  if (warp == 0) {
+  // What the entry warp looks up ahead, while warp 0 still loads the job's pairs: the
+  // page chunks of this rank's first tiles of the group's first member.
+  int pre_b = -1, pre_row = -1;
+  const int chunks = a.box ? kTile / a.box : 32, ahead = a.box ? 32 / chunks : 1;
+  if (warp == kEntryWarp) {
+    int start, members, b = -1;
+    if (a.box && find_job(a, job, nullptr, &start, &members)) b = a.group_seq[start];
+    if (b >= 0 && b < a.B) {
+      const long long key = (rank + static_cast<long long>(lane / chunks) * a.c) * kTile + (lane % chunks) * a.box;
+      pre_b = b;
+      if (key < static_cast<long long>(a.max_pages) * a.P) pre_row = entry_row(a, b, static_cast<int>(key));
+    }
+  } else if (warp == 0) {
     int start, members;
-    const bool some = find_job(a, job, sm, &start, &members);
+    const bool some = find_job(a, job, &sm, &start, &members);
     if (some) load_pairs(a, sm, start, members);
     else if (lane == 0) sm.group = -1;
   } else if (warp == 1 && lane == 0) {
@@ -538,19 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       ++g;
     };
     if (warp == kEntryWarp) {
-      // Entry `key` of sequence b as a row of the pool, or -1.
-      auto entry = [&](int b, int key, int n) {
-        if (key >= n) return -1;
-        const int pg = a.P > 1 ? static_cast<int>(__umulhi(key, a.p_mul) >> a.p_shift) : key;
-        const int id = a.table[static_cast<size_t>(b) * a.max_pages + pg];
-        return id >= 0 && id < a.N ? id * a.P + (key - pg * a.P) : -1;
-      };
+      auto entry = [&](int b, int key, int n) { return key < n ? entry_row(a, b, key) : -1; };
       // This rank's entry tiles i, i + c, .. of sequence b below n.  The page chunks of
       // the next 32 / chunks tiles are looked up at once, a lane each; then one
       // thread walks those tiles (per tile, a warp's lookups, votes and branches paced
       // the loop at 2000 cycles; these take a few dozen instructions).
-      const int chunks = a.box ? kTile / a.box : 32;
-      const int ahead = a.box ? 32 / chunks : 1;
       auto put_tiles = [&](int kind, int u, int m, int b, int i, int n) {
         const int end = static_cast<int>((static_cast<uint32_t>(n) + kTile - 1) / kTile);
         while (ok && i < end) {
@@ -559,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
           if (a.box) {
             const int t = lane / chunks;
             const long long key = (i + static_cast<long long>(t) * a.c) * kTile + (lane % chunks) * a.box;
-            const int row = t < batch && key < n ? entry(b, static_cast<int>(key), n) : -1;
+            int row = -1;
+            if (t < batch && key < n) row = b == pre_b && i == rank ? pre_row : entry_row(a, b, static_cast<int>(key));
             const uint32_t bad = __ballot_sync(0xffffffffu, t < batch && key < n && row < 0);
             good = bad ? (__ffs(bad) - 1) / chunks : batch;
             sm.rows[lane] = row;
@@ -881,30 +904,72 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     // boxes still in flight land within microseconds
     for (const uint64_t t0 = global_ns(); global_ns() - t0 < 200000ull;) {}
   } else if (!idle && warp < kSoftWarps) {
-    // Warpgroup w moves dims [64 w, 64 w + 64) of O to where the key tiles were.
+    // A thread has a row and, in warpgroup w, its dims [64 w, 64 w + 64) of O.
     const int w = warp >> 2, r = (warp & 3) * 32 + lane;
-    if (w == 0) {
-      int t;
-      // (a row's M is set once: whichever parity has it, the other has it or nothing)
-      const float m0 = handed(&sm.m_next[0][r], &t), m1 = handed(&sm.m_next[1][r], &t);
-      sm.m[r] = m0 == -INFINITY ? m1 : m0;
-      sm.l[r] = handed(&sm.l_sum[0][r], &t) + handed(&sm.l_sum[1][r], &t);
-    }
-    uint8_t* dst = &sm.kv[0][0] + r * (kDim * 4);
+    int t;
+    // (a row's M is set once: whichever parity has it, the other has it or nothing)
+    const float m0 = handed(&sm.m_next[0][r], &t), m1 = handed(&sm.m_next[1][r], &t);
+    const float M = m0 == -INFINITY ? m1 : m0;
+    const float l = handed(&sm.l_sum[0][r], &t) + handed(&sm.l_sum[1][r], &t);
     tc_fence_after();
     uint32_t x[64];
     const uint32_t ocol = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO + 64 * w;
     PA_TMEM_LD_X32(ocol, x);
     PA_TMEM_LD_X32(ocol + 32, x + 32);
     tmem_ld_wait();
+    if (a.c > 1) {
+      // to where the key tiles were, for the ranks to join
+      if (w == 0) {
+        sm.m[r] = M;
+        sm.l[r] = l;
+      }
+      uint8_t* dst = &sm.kv[0][0] + r * (kDim * 4);
 #pragma unroll
-    for (int e = 0; e < 64; e += 4)
-      *reinterpret_cast<uint4*>(dst + ((((64 * w + e) >> 2) ^ lane) << 4)) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+      for (int e = 0; e < 64; e += 4)
+        *reinterpret_cast<uint4*>(dst + ((((64 * w + e) >> 2) ^ lane) << 4)) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+    } else {
+      // nothing to join
+      const int u = static_cast<int>((static_cast<uint32_t>(r) * a.h_inv) >> 16);
+      const bool real = r < sm.npair * a.H && sm.pair[min(u, kPairs - 1)].b >= 0;
+      const bool again = real && sm.redo[r];
+      const int h = r - u * a.H;
+      if (real && !again) {
+        const Pair& pr = sm.pair[u];
+        const size_t row = (static_cast<size_t>(pr.b) * a.T + pr.t) * a.H + h;
+        float sc, lse;
+        finish_row(M, l, sm.sink_l2[h], &sc, &lse);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * kDim + 64 * w;
+#pragma unroll
+        for (int e = 0; e < 64; e += 8) {
+          uint4 o;
+          o.x = pack_bf16(__uint_as_float(x[e]) * sc, __uint_as_float(x[e + 1]) * sc);
+          o.y = pack_bf16(__uint_as_float(x[e + 2]) * sc, __uint_as_float(x[e + 3]) * sc);
+          o.z = pack_bf16(__uint_as_float(x[e + 4]) * sc, __uint_as_float(x[e + 5]) * sc);
+          o.w = pack_bf16(__uint_as_float(x[e + 6]) * sc, __uint_as_float(x[e + 7]) * sc);
+          *reinterpret_cast<uint4*>(out + e) = o;
+        }
+        if (a.lse && w == 0) a.lse[row] = lse;
+      }
+      for (uint32_t todo = w == 0 ? __ballot_sync(0xffffffffu, again) : 0u; todo; todo &= todo - 1) {
+        const int rr = (warp & 3) * 32 + __ffs(todo) - 1;
+        const int uu = static_cast<int>((static_cast<uint32_t>(rr) * a.h_inv) >> 16);
+        row_exact(a, sm.pair[uu], rr - uu * a.H, sm.sink_l2[rr - uu * a.H]);
+      }
+    }
+  }
+  if (a.c == 1) {
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kQkWarp) {
+      tc_fence_after();
+      tmem_dealloc(tmem, kTmemCols);
+    }
+    return;
   }
   // The ranks' parts of a row meet at the rank that owns it (128 / c rows each): every
   // rank pushes 16-byte-aligned row blocks to the others (pulling them with loads
   // from distributed shared memory took three times as long).
-  const int per = kTile / a.c, row0 = rank * per;
+  const int per = kTile >> a.log_c, row0 = rank * per;
   uint8_t* const parts = &sm.kv[2][0];
   if (threadIdx.x == 0) mbar_arrive_expect_tx(&sm.joined, (a.c - 1) * per * kDim * 4);
   tc_fence_before();
@@ -946,12 +1011,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   float fi = mi == -INFINITY ? 0.f : ex2(mi - M);
   float L = fi * li;
   for (int y = 1; y < a.c; y <<= 1) L += __shfl_xor_sync(0xffffffffu, L, y);
-  float lse = -INFINITY, sc = 0.f;
-  if (L != 0.f) {
-    const float sg = sm.sink_l2[h_of], X = fmaxf(M, sg), fm = ex2(M - X);
-    sc = __fdiv_rn(fm, fmaf(L, fm, ex2(sg - X)));
-    lse = (M + log2f(L)) * 0.6931471805599453f;
-  }
+  float lse, sc;
+  finish_row(M, L, sm.sink_l2[h_of], &sc, &lse);
   const uint32_t redo_lanes = __ballot_sync(0xffffffffu, real && again);
   bool there = finish;
   if (finish && a.c > 1) there = waitw(&sm.joined, 0, a, abort_flag, 34);
