@@ -11,19 +11,21 @@
 // Key tiles come in three kinds:
 //   shared  128 entries that every row of the job sees, loaded once for all;
 //   own     128 entries of one sequence (its pairs that see equally many share a tile);
-//   window  8 runs of 16 raw tokens, each of one pair.
-// Own and window tiles concern some rows only.  The PV MMA of such a tile writes
+//   runs    8 runs of 16 keys, each of one pair: entries behind its last whole tile,
+//           then raw tokens of its window.
+// Own tiles and runs concern some rows only.  The PV MMA of such a tile writes
 // those rows' lanes alone (its lane mask), so a row's sum holds its own keys
 // and nothing else: an infinity or NaN in one sequence's keys cannot reach
 // another's row as 0 * inf.  Keys a row must not see inside its own tiles are
 // zero-filled in shared memory and get P = 0.
 //
-// Split.  A cluster of c CTAs shares each job: entry tile i goes to rank i % c, each
-// window in equal runs of 16 tokens to all ranks.  The ranks' (O, M, l) meet in
-// distributed shared memory, in rank order, each rank finishing every c-th row.
-// c depends on the cache's capacity alone, tiles sit at multiples of 128 entries,
-// and a row's rescaling depends on the row: its bits do not depend on batch or
-// grouping.
+// Split.  A cluster of c CTAs shares each job: whole entry tile i goes to rank i % c, the
+// 16-key runs behind the last whole tile and those of the window in turn to all
+// ranks (a last tile as a whole would fall to one rank for all of a job's sequences).
+// The ranks' (O, M, l) meet in distributed shared memory, in rank order, each rank
+// finishing 128 / c rows.  c depends on the cache's capacity and H alone, tiles
+// sit at multiples of 128 entries, and a row's stabiliser is its own: its bits do
+// not depend on batch or grouping.
 //
 // Softmax.  A row's stabiliser M is the maximum of its first tile in the rank, and
 // stays: weights 2^(l - M) and their sums keep fp32's (and, in P, bf16's) relative
@@ -33,15 +35,18 @@
 // largest is lost against it anyway.  So once M is there a tile needs no maximum and no
 // word from the tiles before (a running one took a third of a tile's time).
 // P is rounded to bf16 for the MMA (a half step of 2^-9 a weight, of the size
-// of the output's own rounding); the row sum adds the unrounded weights, by tile
-// parity (i / c) % 2.
+// of the output's own rounding); the row sum adds the rounded weights, by tile
+// parity (i / c) % 2, so that what all of a row's weights have in common cancels.
+//
+// Tile order: the runs, the shared tiles, the own ones.
 //
 // Roles (12 warps).  Softmax warpgroups 0 and 1 (warps 0 - 3, 4 - 7) take the even
-// and the odd tiles, a thread a row; S and P are double buffered, O is one.  Warp
-// 8 loads entries: by TMA boxes of a page (or the largest power of two of its rows),
-// row by row where a page is missing; warp 9 window rows, by 16-byte asynchronous
-// copies.  Warp 10 issues QK (a warpgroup's next as soon as it has read the last
-// S), warp 11 PV.
+// and the odd tiles, a thread a row; S and P are double buffered, O is one.  Before
+// that they load Q and the first run tiles, a warp a run, by 16-byte asynchronous
+// copies (one warp took 4700 cycles for a tile); warp 9 loads the further ones.  Warp 8
+// loads entries: by TMA boxes of a page (or the largest power of two of its rows),
+// row by row where a page is missing.  Warp 10 issues QK (a warpgroup's next as soon
+// as it has read the last S), warp 11 PV.
 //
 // All waits are bounded in time and every thread reaches the cluster barriers.
 #include <cuda.h>
@@ -57,40 +62,39 @@ constexpr int kTile = 128, kDim = 128;
 constexpr int kStages = 5;                    // a tile lives ~6700 cycles: load, QK, softmax, PV
 constexpr int kTileBytes = kTile * kDim * 2;
 constexpr int kRegion = kTile * 128;          // the 64-dim half of a tile
-constexpr int kMaxCluster = 8;
 constexpr int kPairs = 16;                    // most pairs of a job
-constexpr int kSoftWarps = 8, kEntryWarp = 8, kWindowWarp = 9, kQkWarp = 10, kPvWarp = 11;
+constexpr int kSoftWarps = 8, kEntryWarp = 8, kRunWarp = 9, kQkWarp = 10, kPvWarp = 11;
 constexpr int kThreads = 384;
+constexpr int kFull = 8 * 33;                 // arrivals that fill a stage: 8 warps' lanes and words
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 256, kColO = 384;   // S, P of tile parity w at 128 w, 256 + 64 w
 constexpr float kMost = 1.2676506e30f;        // 2^100: a row's weights beyond it are done again
 
-enum : int { kShared = 0, kOwn = 1, kWindow = 2, kEnd = 3 };
+enum : int { kShared = 0, kOwn = 1, kRuns = 2, kEnd = 3 };
 
 struct Pair {
   int b, t, n, nw;        // sequence, token; visible entries; window rows (0 .. W)
-  int p;                  // position
+  int p, slot;            // position, its ring slot
 };
-// A tile: its kind; own: the pairs u .. u + m - 1; cnt: keys that are there (shared,
-// own) or runs (window); seg0: the window's first run, an own tile's parity.  One
-// 16-byte word.
+// A tile: its kind; own: the pairs u .. u + m - 1; runs: how many there are, the first's
+// number; an own tile's parity.  One 16-byte word.
 struct __align__(16) Desc {
-  int kind, um, cnt, seg0;
+  int kind, um, runs, at;
   __device__ int u() const { return um & 0xff; }
   __device__ int m() const { return um >> 8; }
 };
-__device__ __forceinline__ Desc make_desc(int kind, int u, int m, int cnt, int seg0) {
-  return Desc{kind, u | (m << 8), cnt, seg0};
+__device__ __forceinline__ Desc make_desc(int kind, int u, int m, int runs, int at) {
+  return Desc{kind, u | (m << 8), runs, at};
 }
 
 struct __align__(1024) Smem {
   uint8_t q[kTileBytes];
   uint8_t kv[kStages][kTileBytes];     // reused at the end: the CTA's O (64 KB), then the ranks' parts of its rows (64 KB)
-  uint64_t kv_full[kStages], kv_empty[kStages], win_go[kStages], q_full, s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t kv_full[kStages], kv_empty[kStages], q_full, s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t drain[2], joined;
   // (tile, value) on its way between the warpgroups: a row's M (by the tile parity it
   // comes from) and sums (by the parity they belong to)
-  unsigned long long m_next[2][kTile], l_sum[2][kTile];
+  unsigned long long m_next[2][kTile], l_sum[3][kTile];     // (the third sum: the runs')
   uint8_t redo[kTile];
   float m[kTile], l[kTile];            // the CTA's, at the end
   uint4 valid[kStages];                // which rows are keys
@@ -98,6 +102,7 @@ struct __align__(1024) Smem {
   Desc desc[kStages];
   float sink_l2[kTile];                // by head
   Pair pair[kPairs];
+  uint4 off[kPairs];                   // lanes that are not the pair's
   int npair;
   int group, tile, shared, leader;
   uint32_t tmem;
@@ -114,7 +119,8 @@ struct Args : PrefixAttnArgs {
   uint32_t h_inv;       // ceil(2^16 / H): r / H = r h_inv >> 16 for r < 128
   int c;                // cluster size
   int ppt;              // pairs a job
-  int win_run;          // window tokens a rank takes of each pair (a multiple of 16)
+  int tail_runs, win_runs;   // 16-key runs that a rank takes of each pair: entries, window
+  int pair_runs, log_room;   // the room they have in the run tiles: a pair lies in one or fills several
   unsigned long long wait_ns;
   unsigned hint_ns;
 };
@@ -221,12 +227,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // D[tmem] += A[tmem] * B[smem]; lanes whose bit is set in `off` are not written.
 __device__ __forceinline__ void mma_ts_lanes(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             const uint32_t off[4]) {
+                                             const uint4& off) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, 1, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
@@ -346,7 +352,7 @@ __device__ void load_pairs(const Args& a, Smem& sm, int o0, int members) {
   const int lead = a.group_seq[o0];
   int n = max(a.group_shared[sm.group], 0);
   if (lane < np) {
-    Pair pr{-1, 0, 0, 0, -1};
+    Pair pr{-1, 0, 0, 0, -1, 0};
     const int i = first + lane;
     const int b = a.group_seq[o0 + i / a.T];
     if (b >= 0 && b < a.B) {
@@ -355,11 +361,15 @@ __device__ void load_pairs(const Args& a, Smem& sm, int o0, int members) {
       const long long p = static_cast<long long>(a.q_pos0[b]) + pr.t;
       pr.p = static_cast<int>(min(p, static_cast<long long>(INT32_MAX)));
       pr.n = visible_entries(a, b, p);
+      pr.slot = p < 0 || a.W == 0 ? 0 : static_cast<int>(static_cast<uint32_t>(pr.p) % static_cast<uint32_t>(a.raw_cap));
       pr.nw = p < 0 ? 0 : static_cast<int>(min(static_cast<long long>(a.W), p + 1));
     } else {
       atomicCAS(a.status, 0, CSA_ERR_INVALID_ARG | (4 << 8));
     }
     sm.pair[lane] = pr;
+    uint32_t off[4];
+    lanes_off(off, lane * a.H, lane * a.H + a.H);
+    sm.off[lane] = make_uint4(off[0], off[1], off[2], off[3]);
     n = min(n, pr.n);
   } else if (lane == 31) {       // (a job has 16 pairs at most)
     n = lead < 0 || lead >= a.B
@@ -483,9 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     else if (lane == 0) sm.group = -1;
   } else if (warp == 1 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.kv_full[s], 33);
+      mbar_init(&sm.kv_full[s], kFull);
       mbar_init(&sm.kv_empty[s], 1);
-      mbar_init(&sm.win_go[s], 1);
     }
     mbar_init(&sm.q_full, 32 * kSoftWarps);
     for (int w = 0; w < 2; ++w) {
@@ -511,105 +520,113 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   const bool idle = sm.group < 0;      // the same in every CTA of the cluster
-  const int segs = max(a.win_run / 16, 1);
+  const int room = a.pair_runs, run_tiles = idle ? 0 : (sm.npair * room + 7) / 8;
+  // Where row x (0 .. 15) of run `run` lies, or null.
+  auto run_row = [&](int run, int x) -> const __nv_bfloat16* {
+    // (a pair has a power of two of runs in a tile, or whole tiles)
+    const int u = room <= 8 ? run >> a.log_room : run / room, i = run - u * room;
+    if (u >= sm.npair) return nullptr;
+    const Pair pr = sm.pair[u];
+    if (i < a.tail_runs) {
+      const int key = (pr.n & ~(kTile - 1)) + (rank + i * a.c) * 16 + x;
+      const int y = key < pr.n ? entry_row(a, pr.b, key) : -1;
+      return y >= 0 ? static_cast<const __nv_bfloat16*>(a.pool) + static_cast<size_t>(y) * kDim : nullptr;
+    }
+    // how many tokens before the query's own
+    const int back = (rank + (i - a.tail_runs) * a.c) * 16 + x;
+    if (i >= a.tail_runs + a.win_runs || back >= pr.nw) return nullptr;
+    const int slot = pr.slot - back + (back > pr.slot ? a.raw_cap : 0);
+    return static_cast<const __nv_bfloat16*>(a.kv_raw) + (static_cast<size_t>(pr.b) * a.raw_cap + slot) * kDim;
+  };
   // the first entry tile of this rank behind the shared ones
   const int own0 = idle ? 0 : sm.shared + ((rank - sm.shared) & (a.c - 1));
 
-  if (!idle && (warp == kEntryWarp || warp == kWindowWarp)) {
+  if (!idle && (warp == kEntryWarp || warp == kRunWarp)) {
     // ================================================================= producers
     const int half = lane >> 4, c = lane & 15;
     bool ok = true;
-    // The entry tiles come first, then the window's, then the end.  The entry warp sees
-    // every stage through its uses (an mbarrier tells a phase from the next alone,
-    // so a waiter must not skip one) and opens the window warp's stages to it.
-    int mine = 0;
-    if (lane < sm.npair && !joined(sm, lane)) mine = tiles_of(own0, sm.pair[lane].n, a.log_c);
-    const int entry_tiles = tiles_of(rank, sm.shared * kTile, a.log_c) + __reduce_add_sync(0xffffffffu, mine);
-    const int win_tiles = rank * a.win_run < a.W ? (sm.npair * segs + 7) / 8 : 0;
-    int g = warp == kEntryWarp ? 0 : entry_tiles;
+    // The first kStages run tiles are the softmax warps'.  Both warps here see every
+    // stage through its uses (an mbarrier tells a phase from the next alone, so a
+    // waiter must not skip one).
+    int g = kStages;
     auto stage_free = [&]() {
-      const int stage = g % kStages, use = g / kStages;
-      if (use < 1) return true;
-      if (warp == kEntryWarp) return waitw(&sm.kv_empty[stage], (use - 1) & 1, a, abort_flag, 20);
-      // the stage's first use by a window slot that waits
-      const int first = max(1, (entry_tiles - stage + kStages - 1) / kStages);
-      return waitw(&sm.win_go[stage], (use - first) & 1, a, abort_flag, 32);
+      const int use = g / kStages;
+      return use < 1 || waitw(&sm.kv_empty[g % kStages], (use - 1) & 1, a, abort_flag, 20);
     };
-    // One tile row by row: src(r) gives the row of `from` for tile row r, or -1.
-    auto put = [&](const Desc& d, const void* from, int rows, auto&& src) {
+    // One tile row by row: src(r) gives where tile row r's key lies, or null.  Runs of 16
+    // rows without a key are left out (and by the PV).
+    auto put = [&](const Desc& d, int rows, auto&& src) {
       const int stage = g % kStages;
-      int x[4];
-      uint32_t bits[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = 32 * i < rows ? src(32 * i + lane) : -1;
-        bits[i] = __ballot_sync(0xffffffffu, x[i] >= 0);
-      }
       if (!stage_free()) { ok = false; return; }
-      const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(from) + c * 8;
-      const uint32_t dbase = smem_u32(sm.kv[stage]) + (c >> 3) * kRegion + half * 128;
+      const char* none = static_cast<const char*>(a.pool);
+      uint32_t dst = smem_u32(sm.kv[stage]) + (c >> 3) * kRegion + half * 128;
       const uint32_t cx = static_cast<uint32_t>((c & 7) ^ half);
+      uint4 bits = make_uint4(0u, 0u, 0u, 0u);
+      // (rolled: code that runs once or twice is paid for in instruction fetches)
+#pragma unroll 1
+      for (int i = 0; 32 * i < rows; ++i, dst += 32 * 128) {
+        const unsigned long long x = reinterpret_cast<unsigned long long>(src(32 * i + lane));
+        const uint32_t word = __ballot_sync(0xffffffffu, x != 0ull);
+        if (i == 0) bits.x = word;
+        else if (i == 1) bits.y = word;
+        else if (i == 2) bits.z = word;
+        else bits.w = word;
+#pragma unroll 1
+        for (int run = 0; run < 2; ++run) {
+          if (!((word >> (16 * run)) & 0xffffu)) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (32 * i >= rows) break;
-#pragma unroll 8
-        for (int j = 0; j < 16; ++j) {
-          const int y = __shfl_sync(0xffffffffu, x[i], 2 * j + half);
-          const uint32_t dst = dbase + (16 * i + j) * 256 + ((cx ^ static_cast<uint32_t>((2 * j) & 7)) << 4);
-          cp_async16(dst, base + static_cast<size_t>(max(y, 0)) * kDim, y >= 0 ? 16u : 0u);
+          for (int j = 0; j < 8; ++j) {
+            const unsigned long long y = __shfl_sync(0xffffffffu, x, 16 * run + 2 * j + half);
+            cp_async16(dst + (8 * run + j) * 256 + ((cx ^ static_cast<uint32_t>((2 * j) & 7)) << 4),
+                       (y ? reinterpret_cast<const char*>(y) : none) + c * 16, y ? 16u : 0u);
+          }
         }
       }
       cp_async_mbar_arrive(&sm.kv_full[stage]);
       if (lane == 0) {
-        sm.valid[stage] = make_uint4(bits[0], bits[1], bits[2], bits[3]);
+        sm.valid[stage] = bits;
         sm.desc[stage] = d;
-        mbar_arrive(&sm.kv_full[stage]);
+        mbar_arrive_n(&sm.kv_full[stage], kFull - 32);
       }
       ++g;
     };
+    auto pool_row = [&](int b, int key) -> const void* {
+      const int x = entry_row(a, b, key);
+      return x >= 0 ? static_cast<const __nv_bfloat16*>(a.pool) + static_cast<size_t>(x) * kDim : nullptr;
+    };
     if (warp == kEntryWarp) {
-      auto entry = [&](int b, int key, int n) { return key < n ? entry_row(a, b, key) : -1; };
-      // This rank's entry tiles i, i + c, .. of sequence b below n.  The page chunks of
+      // This rank's entry tiles i, i + c, .. of sequence b below tile `end`.  The page chunks of
       // the next 32 / chunks tiles are looked up at once, a lane each; then one
       // thread walks those tiles (per tile, a warp's lookups, votes and branches paced
       // the loop at 2000 cycles; these take a few dozen instructions).
-      auto put_tiles = [&](int kind, int u, int m, int b, int i, int n) {
-        const int end = static_cast<int>((static_cast<uint32_t>(n) + kTile - 1) / kTile);
+      auto put_tiles = [&](int kind, int u, int m, int b, int i, int end) {
         while (ok && i < end) {
           const int batch = min(ahead, (end - i + a.c - 1) >> a.log_c);
           int good = 0;                  // tiles before the first with a missing page
           if (a.box) {
             const int t = lane / chunks;
-            const long long key = (i + static_cast<long long>(t) * a.c) * kTile + (lane % chunks) * a.box;
             int row = -1;
-            if (t < batch && key < n) row = b == pre_b && i == rank ? pre_row : entry_row(a, b, static_cast<int>(key));
-            const uint32_t bad = __ballot_sync(0xffffffffu, t < batch && key < n && row < 0);
+            if (t < batch)
+              row = b == pre_b && i == rank ? pre_row : entry_row(a, b, (i + t * a.c) * kTile + (lane % chunks) * a.box);
+            const uint32_t bad = __ballot_sync(0xffffffffu, t < batch && row < 0);
             good = bad ? (__ffs(bad) - 1) / chunks : batch;
             sm.rows[lane] = row;
             __syncwarp();
             bool fine = true;
             if (elect_one()) {
-              int stage = g % kStages, use = g / kStages, key0 = i * kTile;
-              for (int k = 0; k < good; ++k, key0 += a.c * kTile) {
+              int stage = g % kStages, use = g / kStages, tile = i;
+              for (int k = 0; k < good; ++k, tile += a.c) {
                 if (use >= 1 && !wait1(&sm.kv_empty[stage], (use - 1) & 1, a, abort_flag, 20)) { fine = false; break; }
-                const int cnt = min(kTile, n - key0);
-                uint4 bits = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
-                if (cnt < kTile) {
-                  uint32_t off[4];
-                  lanes_off(off, 0, cnt);
-                  bits = make_uint4(~off[0], ~off[1], ~off[2], ~off[3]);
-                }
-                sm.valid[stage] = bits;
-                sm.desc[stage] = make_desc(kind, u, m, cnt, (key0 / kTile >> a.log_c) & 1);
-                const int boxes = (cnt + a.box - 1) / a.box;
-                mbar_expect_tx(&sm.kv_full[stage], boxes * a.box * kDim * 2);
+                sm.valid[stage] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+                sm.desc[stage] = make_desc(kind, u, m, 0, (tile >> a.log_c) & 1);
+                mbar_expect_tx(&sm.kv_full[stage], kTileBytes);
                 uint32_t dst = smem_u32(sm.kv[stage]);
-                for (int x = 0; x < boxes; ++x, dst += a.box * 128) {
+                for (int x = 0; x < chunks; ++x, dst += a.box * 128) {
                   const int y = sm.rows[k * chunks + x];
                   tma_load_2d(dst, reinterpret_cast<uint64_t>(&pool_map), 0, y, &sm.kv_full[stage]);
                   tma_load_2d(dst + kRegion, reinterpret_cast<uint64_t>(&pool_map), 64, y, &sm.kv_full[stage]);
                 }
-                mbar_arrive_n(&sm.kv_full[stage], 33);
+                mbar_arrive_n(&sm.kv_full[stage], kFull);
                 if (++stage == kStages) { stage = 0; ++use; }
               }
             }
@@ -619,38 +636,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
           }
           if (ok && good < batch) {
             const int key0 = i * kTile;
-            put(make_desc(kind, u, m, min(kTile, n - key0), (i >> a.log_c) & 1), a.pool, kTile, [&](int r) { return entry(b, key0 + r, n); });
+            put(make_desc(kind, u, m, 0, (i >> a.log_c) & 1), kTile, [&](int r) { return pool_row(b, key0 + r); });
             i += a.c;
           }
         }
       };
-      put_tiles(kShared, 0, 0, sm.leader, rank, sm.shared * kTile);
+      for (; ok && g < run_tiles; ++g) ok = stage_free();
+      g = run_tiles;
+      put_tiles(kShared, 0, 0, sm.leader, rank, sm.shared);
       for (int u = 0; u < sm.npair && ok;) {
         int m = 1;
         while (u + m < sm.npair && joined(sm, u + m)) ++m;
-        put_tiles(kOwn, u, m, sm.pair[u].b, own0, sm.pair[u].n);
+        put_tiles(kOwn, u, m, sm.pair[u].b, own0, sm.pair[u].n / kTile);
         u += m;
       }
-      for (; ok && g <= entry_tiles + win_tiles; ++g) {
-        if (g < kStages) continue;
-        ok = stage_free();
-        if (ok && lane == 0) mbar_arrive(&sm.win_go[g % kStages]);
-        __syncwarp();
-      }
+      if (ok) put(make_desc(kEnd, 0, 0, 0, 0), 0, [](int) -> const void* { return nullptr; });
       cp_async_wait<0>();
     } else {
-      for (int t = 0; ok && t < win_tiles; ++t) {
-        const int k0 = 8 * t, runs = min(8, sm.npair * segs - k0);
-        put(make_desc(kWindow, 0, 0, runs, k0), a.kv_raw, runs * 16, [&](int r) {
-          const int sg = k0 + (r >> 4), u = sg / segs;
-          if (u >= sm.npair) return -1;
-          const Pair pr = sm.pair[u];
-          // how many tokens before the query's own
-          const int back = rank * a.win_run + (sg - u * segs) * 16 + (r & 15);
-          return back < pr.nw ? pr.b * a.raw_cap + (pr.p - back) % a.raw_cap : -1;
-        });
+      while (ok && g < run_tiles) {
+        const int at = 8 * g, runs = min(8, sm.npair * room - at);
+        put(make_desc(kRuns, 0, 0, runs, at), runs * 16, [&](int r) -> const void* { return run_row(at + (r >> 4), r & 15); });
       }
-      if (ok) put(make_desc(kEnd, 0, 0, 0, 0), a.pool, 0, [](int) { return -1; });
       cp_async_wait<0>();
     }
   } else if (!idle && warp == kQkWarp) {
@@ -713,19 +719,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
 #pragma unroll
           for (int j = 0; j < kTile / 16; ++j) mma_ts(ocol, pcol + 8 * j, kd + j * (2048 >> 4), idesc_pv);
         } else {
-          const bool win = d.kind == kWindow;
-          const int steps = win ? d.cnt : (d.cnt + 15) / 16, m = win ? 1 : d.m();
-          int u = win ? d.seg0 / segs : d.u();
-          int left = win ? segs - d.seg0 % segs : kTile;
-          uint32_t off[4];
-          lanes_off(off, u * a.H, (u + m) * a.H);
-          for (int j = 0; j < steps; ++j) {
+          // The rows' lanes alone; runs without a key are left out.
+          const bool own = d.kind == kOwn;
+          const uint4 bits = sm.valid[stage];
+          uint32_t todo = own ? 0xffu : (1u << d.runs) - 1u;
+          if (!(bits.x & 0xffffu)) todo &= ~1u;
+          if (!(bits.x >> 16)) todo &= ~2u;
+          if (!(bits.y & 0xffffu)) todo &= ~4u;
+          if (!(bits.y >> 16)) todo &= ~8u;
+          if (!(bits.z & 0xffffu)) todo &= ~16u;
+          if (!(bits.z >> 16)) todo &= ~32u;
+          if (!(bits.w & 0xffffu)) todo &= ~64u;
+          if (!(bits.w >> 16)) todo &= ~128u;
+          uint4 off = sm.off[own ? d.u() : 0];
+          for (int x = own ? d.u() + 1 : 0; own && x < d.u() + d.m(); ++x) {
+            const uint4 more = sm.off[x];
+            off = make_uint4(off.x & more.x, off.y & more.y, off.z & more.z, off.w & more.w);
+          }
+          while (todo) {
+            const int j = __ffs(todo) - 1;
+            todo &= todo - 1;
+            if (!own) off = sm.off[room <= 8 ? (d.at + j) >> a.log_room : d.at / room];
             mma_ts_lanes(ocol, pcol + 8 * j, kd + j * (2048 >> 4), idesc_pv, off);
-            if (--left == 0) {        // the next run is the next pair's
-              ++u;
-              left = segs;
-              lanes_off(off, u * a.H, (u + m) * a.H);
-            }
           }
         }
         tc_commit(&sm.kv_empty[stage]);
@@ -764,6 +779,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         cp_async16(dst + y * 128 + (((c & 7) ^ (y & 7)) << 4), q + row * kDim, some ? 16u : 0u);
       }
       cp_async_commit();
+      // The first run tiles: run `warp` of each, 16 lanes a row.
+#pragma unroll 1
+      for (int t = 0; t < min(run_tiles, kStages); ++t) {
+        const unsigned long long x = reinterpret_cast<unsigned long long>(run_row(8 * t + warp, lane & 15));
+        const uint32_t word = __ballot_sync(0xffffffffu, x != 0ull) & 0xffffu;
+        if (word) {
+          const int half = lane >> 4;
+          const uint32_t to = smem_u32(sm.kv[t]) + (c >> 3) * kRegion + (16 * warp + half) * 128;
+          const uint32_t cx = static_cast<uint32_t>((c & 7) ^ half);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const unsigned long long y = __shfl_sync(0xffffffffu, x, 2 * j + half);
+            cp_async16(to + j * 256 + ((cx ^ static_cast<uint32_t>((2 * j) & 7)) << 4),
+                       (y ? reinterpret_cast<const char*>(y) : static_cast<const char*>(a.pool)) + c * 16, y ? 16u : 0u);
+          }
+        }
+        cp_async_mbar_arrive(&sm.kv_full[t]);
+        if (lane == 0) {
+          reinterpret_cast<uint16_t*>(&sm.valid[t])[warp] = static_cast<uint16_t>(word);
+          if (warp == 0) sm.desc[t] = make_desc(kRuns, 0, 0, min(8, sm.npair * room - 8 * t), 8 * t);
+          mbar_arrive(&sm.kv_full[t]);
+        }
+      }
+      cp_async_commit();
       uint32_t z[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) z[e] = 0u;
@@ -773,8 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       tc_fence_before();
       hand_over(&sm.m_next[w][r], -1, -INFINITY);
       hand_over(&sm.l_sum[w][r], -1, 0.f);
-      if (w == 0) sm.redo[r] = 0;
-      cp_async_wait<0>();
+      if (w == 0) {
+        hand_over(&sm.l_sum[2][r], -1, 0.f);
+        sm.redo[r] = 0;
+      }
+      cp_async_wait<1>();
       if (a.negate) {
         for (int i = 0; i < kTile / kSoftWarps / 2; ++i) {
           const int y = (threadIdx.x >> 4) + 2 * kSoftWarps * i;
@@ -787,7 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     }
     const int u = r < rows ? static_cast<int>((static_cast<uint32_t>(r) * a.h_inv) >> 16) : -1;
     const float sl2 = a.scale_log2;
-    const int shared_tiles = tiles_of(rank, sm.shared * kTile, a.log_c);
+    const int own_at = run_tiles + tiles_of(rank, sm.shared * kTile, a.log_c);      // the first own tile
+    const int p_of = (run_tiles + w) & 1;      // the parity of this warpgroup's shared tiles
     float M = -INFINITY, l = 0.f;      // -inf: not set yet
     bool first_known = false;
     int stage = w;                       // g % kStages
@@ -808,12 +851,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       int lo = 0, hi = kTile;
       if (d.kind == kOwn) {
         mine = u >= d.u() && u < d.u() + d.m();
-      } else if (d.kind == kWindow) {
-        lo = min(max(u * segs - d.seg0, 0), 8) * 16;
-        hi = min(max((u + 1) * segs - d.seg0, 0), 8) * 16;
+      } else if (d.kind == kRuns) {
+        lo = min(max(u * room - d.at, 0), 8) * 16;
+        hi = min(max((u + 1) * room - d.at, 0), 8) * 16;
         mine = u >= 0 && hi > lo;
       }
-      const bool full = d.kind == kShared && (bits.x & bits.y & bits.z & bits.w) == 0xffffffffu;
+      // every row that counts sees every column
+      const bool full = d.kind != kRuns && (bits.x & bits.y & bits.z & bits.w) == 0xffffffffu;
       const bool any = __any_sync(0xffffffffu, mine);
       tmem_ld_wait();
       if (end) break;
@@ -828,33 +872,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         for (int e = 0; e < 128; ++e)
           if (!((see[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;   // -inf: weight 0
       }
-      // Where the rank has shared tiles, the first sets every row's M; else a row's comes
-      // with its first own tile, and whatever is set goes along from tile to tile.
+      // A row's M comes with the first tile in which it sees a key; what is set goes along
+      // from tile to tile until all of the warp's rows have theirs.
       if (!first_known) {
         if (g > 0 && !take(&sm.m_next[w ^ 1][r], g - 1, &M, a, abort_flag, 23)) break;
+        if (u < 0) M = 0.f;
         const bool sets = mine && M == -INFINITY;
         if (__any_sync(0xffffffffu, sets)) {
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < 128; e += 2)
             mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-          const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], -INFINITY) * sl2;   // (NaN stays)
-          if (sets) M = mx == -INFINITY ? 0.f : mx;
+          // (NaN stays; -inf, where it sees nothing here, sets nothing)
+          if (sets) M = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], -INFINITY) * sl2;
         }
         hand_over(&sm.m_next[w][r], g, M);
-        first_known = rank < sm.shared;
+        first_known = __all_sync(0xffffffffu, M != -INFINITY);
       }
       // P's buffer is free once the PV two tiles back has read it
       if (g >= 2 && !waitw(&sm.pv_done[w], (k - 1) & 1, a, abort_flag, 29)) break;
       tc_fence_after();
-      if (d.kind == kOwn && (d.cnt & 15)) {
-        // the tile's rows behind the last key, in its 16: P is 0 there, but what the page
-        // holds may be NaN
-        for (int i = d.cnt * 16 + (threadIdx.x & 127); i < (d.cnt + 15) / 16 * 256; i += 128)
-          *reinterpret_cast<uint4*>(sm.kv[stage] + ((i >> 3) & 1) * kRegion + (i >> 4) * 128 +
-                                    (((i & 7) ^ ((i >> 4) & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async();
-      }
       float sum = 0.f;
       if (any) {
         const float negM = M == -INFINITY ? 0.f : -M;
@@ -868,9 +905,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
             const float x1 = ex2(fmaf(__uint_as_float(v[cc + e + 1]), sl2, negM));
             const float x2 = ex2(fmaf(__uint_as_float(v[cc + e + 2]), sl2, negM));
             const float x3 = ex2(fmaf(__uint_as_float(v[cc + e + 3]), sl2, negM));
-            s0 += x0; s1 += x1; s2 += x2; s3 += x3;
-            pk[e >> 1] = pack_bf16(x0, x1);
-            pk[(e >> 1) + 1] = pack_bf16(x2, x3);
+            const uint32_t p0 = pack_bf16(x0, x1), p1 = pack_bf16(x2, x3);
+            // (the weights that PV multiplies: numerator and denominator see one rounding)
+            s0 += __uint_as_float(p0 << 16);
+            s1 += __uint_as_float(p0 & 0xffff0000u);
+            s2 += __uint_as_float(p1 << 16);
+            s3 += __uint_as_float(p1 & 0xffff0000u);
+            pk[e >> 1] = p0;
+            pk[(e >> 1) + 1] = p1;
           }
           tmem_st16(pcol + (cc >> 1), pk);
         }
@@ -880,24 +922,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       tc_fence_before();
       mbar_arrive(&sm.p_full[w]);
       if (sum > kMost) sm.redo[r] = 1;
-      // Row sums.  Shared tile g belongs to parity g % 2, so each warpgroup has
-      // its own; behind them a tile may come to either, and both go along.
-      if (d.kind == kShared) {
+      // Row sums: the runs' in their order, the entries' by parity (i / c) % 2.  Shared
+      // tiles alternate between the warpgroups, so each has a parity of its own;
+      // behind them a tile may come to either, and both go along.
+      if (d.kind == kRuns) {
+        float run = 0.f;
+        if (g > 0 && !take(&sm.l_sum[2][r], g - 1, &run, a, abort_flag, 35)) break;
+        hand_over(&sm.l_sum[2][r], g, run + sum);
+      } else if (d.kind == kShared) {
         l += sum;
-        hand_over(&sm.l_sum[w][r], g, l);
+        hand_over(&sm.l_sum[p_of][r], g, l);
       } else {
         float own = l, other = 0.f;
-        if (g > 0) {
-          if (!take(&sm.l_sum[w ^ 1][r], g - 1, &other, a, abort_flag, 30)) break;
-          if (g > shared_tiles && !take(&sm.l_sum[w][r], g - 1, &own, a, abort_flag, 33)) break;
+        if (g > run_tiles) {
+          if (!take(&sm.l_sum[p_of ^ 1][r], g - 1, &other, a, abort_flag, 30)) break;
+          if (g > own_at && !take(&sm.l_sum[p_of][r], g - 1, &own, a, abort_flag, 33)) break;
         }
-        // an own tile's parity, the window's is 1
-        const int p = d.kind == kOwn ? d.seg0 : 1;
-        if (p == w) own += sum; else other += sum;
-        hand_over(&sm.l_sum[w ^ 1][r], g, other);
-        hand_over(&sm.l_sum[w][r], g, own);
+        if (d.at == p_of) own += sum; else other += sum;
+        hand_over(&sm.l_sum[p_of ^ 1][r], g, other);
+        hand_over(&sm.l_sum[p_of][r], g, own);
       }
     }
+    cp_async_wait<0>();
   }
   __syncthreads();
   if (*abort_flag) {
@@ -910,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     // (a row's M is set once: whichever parity has it, the other has it or nothing)
     const float m0 = handed(&sm.m_next[0][r], &t), m1 = handed(&sm.m_next[1][r], &t);
     const float M = m0 == -INFINITY ? m1 : m0;
-    const float l = handed(&sm.l_sum[0][r], &t) + handed(&sm.l_sum[1][r], &t);
+    const float l = (handed(&sm.l_sum[0][r], &t) + handed(&sm.l_sum[1][r], &t)) + handed(&sm.l_sum[2][r], &t);
     tc_fence_after();
     uint32_t x[64];
     const uint32_t ocol = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO + 64 * w;
@@ -1095,7 +1141,7 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   if (a.N == 0) a.box = 0;
   if (a.box && !make_pool_map(&map, a.pool, static_cast<uint64_t>(a.N) * a.P, a.box)) return CSA_ERR_CUDA;
   CSA_REQUIRE(static_cast<long long>(a.N) * a.P < (1ll << 31), CSA_ERR_UNSUPPORTED);
-  CSA_REQUIRE(a.W == 0 || static_cast<long long>(a.B) * a.raw_cap < (1ll << 31), CSA_ERR_UNSUPPORTED);
+  CSA_REQUIRE(a.W == 0 || static_cast<long long>(a.B) * a.raw_cap < (1ll << 31) - 2, CSA_ERR_UNSUPPORTED);
   a.ppt = 128 / a.H < kPairs ? 128 / a.H : kPairs;
   // Ranks for the longest sequence that the cache can hold, two entry tiles each at
   // least.  Few heads make few jobs, so up to eight ranks; many heads make a job
@@ -1111,7 +1157,14 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   // above P, ceil(2^(31 + s) / P) fits 32 bits and errs by less than 2^s.
   a.p_shift = a.P > 1 ? 31 - __builtin_clz(static_cast<unsigned>(a.P - 1)) : 0;      // s - 1
   a.p_mul = a.P > 1 ? static_cast<uint32_t>(((1ull << (32 + a.p_shift)) + a.P - 1) / a.P) : 0;
-  a.win_run = ((a.W + a.c - 1) / a.c + 15) / 16 * 16;
+  a.tail_runs = 8 / a.c;
+  a.win_runs = ((a.W + 15) / 16 + a.c - 1) / a.c;
+  // room for them: a power of two below 8 or a multiple of it, so that a pair's runs do
+  // not straddle a tile's end (its first tile sets its rows' stabiliser)
+  a.pair_runs = 1;
+  while (a.pair_runs < 8 && a.pair_runs < a.tail_runs + a.win_runs) a.pair_runs *= 2;
+  a.log_room = 31 - __builtin_clz(static_cast<unsigned>(a.pair_runs));
+  if (a.pair_runs < a.tail_runs + a.win_runs) a.pair_runs = (a.tail_runs + a.win_runs + 7) / 8 * 8;
   int dev = 0;
   cudaGetDevice(&dev);
   const long long pairs = static_cast<long long>(a.n_seq) * a.T;

@@ -116,6 +116,8 @@ CASES = {
                     sink=False),
     "long": dict(groups=[([0], 0), ([1, 2], 4096)], n=[5000, 4097, 4200], T=1, H=64, D=128, m=128, P=64, W=128,
                  dt="bf16"),
+    "odd_window": dict(groups=[([3, 0, 1, 4, 5, 2], 0)], n=[3, 0, 1, 5, 140, 2], T=1, H=16, D=128, m=128, P=16, W=100,
+                       dt="bf16"),
     "wide_window": dict(groups=[([0, 1], 64)], n=[64, 80], T=2, H=16, D=128, m=128, P=64, W=700, dt="bf16"),
     "many_tokens": dict(groups=[([0, 1], 64)], n=[64, 70], T=37, H=8, D=128, m=4, P=16, W=30, dt="bf16"),
     "big_logits": dict(groups=[([0, 1, 2], 256)], n=[256, 500, 900], T=1, H=16, D=128, m=128, P=64, W=128, dt="bf16",
@@ -134,7 +136,7 @@ def test_against_softmax(mods, name):
     b.check(out, lse)
 
 
-@pytest.mark.parametrize("name", ["shared_h16", "shared_h128", "odd_heads", "f32"])
+@pytest.mark.parametrize("name", ["shared_h16", "shared_h128", "odd_heads", "f32", "odd_window", "one_head"])
 def test_rows_do_not_depend_on_grouping_or_batch(mods, name):
     """Every grouping of the batch, and each sequence in a call of its own, gives
     the same bits."""
@@ -211,6 +213,29 @@ def test_bad_pages_are_skipped(mods, dt):
         assert rows
     out, lse = b.run(mods)
     b.keys = lambda i, t: keys[i]
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_logits_far_below_zero(mods, dt):
+    """All of a row's logits near -300: parts of the split that see none of its keys
+    do not set its scale."""
+    b = Batch([([0, 1], 128)], [700, 130], 1, 16, 128, 128, 64, 5, dt, seed=8, sink=False)
+    k = torch.randn(128, generator=torch.Generator().manual_seed(1)) * 4
+    b.pool[:] = (k + 0.05 * b.pool.float()).to(b.pool.dtype)
+    b.ring[:] = (k + 0.05 * b.ring.float()).to(b.ring.dtype)
+    b.q[:] = (-2 * k + 0.05 * b.q.float()).to(b.q.dtype)
+    b.pool[b.rows[1][:2]] = b.pool[b.rows[0][:2]] = float("-inf")     # (never seen below)
+    b.table[:, :2] = -1
+    keys = {}
+    for i in range(2):
+        n = (b.pos[i] + 1) // b.m
+        win = [j % b.cap for j in range(b.pos[i] - b.W + 1, b.pos[i] + 1)]
+        ent = b.pool[b.rows[i]].reshape(-1, b.D)[128:n]
+        keys[i] = np64(torch.cat([ent, b.ring[i, win]]))
+    out, lse = b.run(mods)
+    b.keys = lambda i, t: keys[i]
+    assert lse.max() < -200
     b.check(out, lse)
 
 
