@@ -35,8 +35,9 @@
 // largest is lost against it anyway.  So once M is there a tile needs no maximum and no
 // word from the tiles before (a running one took a third of a tile's time).
 // P is rounded to bf16 for the MMA (a half step of 2^-9 a weight, of the size
-// of the output's own rounding); the row sum adds the rounded weights, by tile
-// parity (i / c) % 2, so that what all of a row's weights have in common cancels.
+// of the output's own rounding).  A row has two sums of its weights, by tile parity
+// (i / c) % 2: as rounded, the output's denominator, so that what all of a row's
+// weights have in common cancels; and in fp32 before it, for lse.
 //
 // Tile order: the runs, the shared tiles, the own ones.
 //
@@ -94,9 +95,11 @@ struct __align__(1024) Smem {
   uint64_t drain[2], joined;
   // (tile, value) on its way between the warpgroups: a row's M (by the tile parity it
   // comes from) and sums (by the parity they belong to)
-  unsigned long long m_next[2][kTile], l_sum[3][kTile];     // (the third sum: the runs')
+  unsigned long long m_next[2][kTile];
+  ulonglong2 l_sum[3][kTile];          // rounded and exact (the third: the runs')
   uint8_t redo[kTile];
-  float m[kTile], l[kTile];            // the CTA's, at the end
+  float m[kTile];                      // the CTA's, at the end
+  float2 l[kTile];
   uint4 valid[kStages];                // which rows are keys
   int rows[32];                        // page chunks on their way to the boxes
   Desc desc[kStages];
@@ -174,9 +177,23 @@ __device__ __forceinline__ float handed(const unsigned long long* slot, int* til
   *tile = static_cast<int>(v >> 32);
   return __uint_as_float(static_cast<uint32_t>(v));
 }
+// Two values, each with its tag (*tile: -2 while the tags differ).
+__device__ __forceinline__ void hand_over(ulonglong2* slot, int tile, float2 x) {
+  const unsigned long long tag = static_cast<unsigned long long>(static_cast<uint32_t>(tile)) << 32;
+  asm volatile("st.volatile.shared.v2.b64 [%0], {%1, %2};" ::"r"(smem_u32(slot)), "l"(tag | __float_as_uint(x.x)),
+               "l"(tag | __float_as_uint(x.y))
+               : "memory");
+}
+__device__ __forceinline__ float2 handed(const ulonglong2* slot, int* tile) {
+  unsigned long long v, w;
+  asm volatile("ld.volatile.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v), "=l"(w) : "r"(smem_u32(slot)) : "memory");
+  *tile = (v >> 32) == (w >> 32) ? static_cast<int>(v >> 32) : -2;
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(w)));
+}
 // Bounded wait of a warp for its rows' values of `tile`.
-__device__ __forceinline__ bool take(const unsigned long long* slot, int tile, float* x, const Args& a,
-                                     volatile int* abort_flag, int site) {
+template <typename Slot, typename Value>
+__device__ __forceinline__ bool take(const Slot* slot, int tile, Value* x, const Args& a, volatile int* abort_flag,
+                                     int site) {
   int t;
   *x = handed(slot, &t);
   if (__all_sync(0xffffffffu, t == tile)) return true;
@@ -204,6 +221,15 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// (x0, x1) += (y0, y1) on the packed fp32 pipe
+__device__ __forceinline__ void add2(float2& x, float y0, float y1) {
+  asm("{\n\t.reg .b64 rx, ry;\n\t"
+      "mov.b64 rx, {%0, %1};\n\tmov.b64 ry, {%2, %3};\n\t"
+      "add.rn.f32x2 rx, rx, ry;\n\tmov.b64 {%0, %1}, rx;\n\t}"
+      : "+f"(x.x), "+f"(x.y)
+      : "f"(y0), "f"(y1));
+}
+__device__ __forceinline__ float2 operator+(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -436,14 +462,15 @@ __device__ __noinline__ void row_exact(const Args& a, const Pair& pr, int h, flo
   if (a.lse && lane == 0) a.lse[row] = lse;
 }
 
-// The factor of O and the lse of a row with stabiliser M and sum L (log2 domain).
-__device__ __forceinline__ void finish_row(float M, float L, float sink_l2, float* sc, float* lse) {
+// The factor of O and the lse of a row with stabiliser M and sums L, rounded and exact
+// (log2 domain).
+__device__ __forceinline__ void finish_row(float M, float2 L, float sink_l2, float* sc, float* lse) {
   *sc = 0.f;
   *lse = -INFINITY;
-  if (L != 0.f) {
+  if (L.x != 0.f) {
     const float X = fmaxf(M, sink_l2), fm = ex2(M - X);
-    *sc = __fdiv_rn(fm, fmaf(L, fm, ex2(sink_l2 - X)));
-    *lse = (M + log2f(L)) * 0.6931471805599453f;
+    *sc = __fdiv_rn(fm, fmaf(L.x, fm, ex2(sink_l2 - X)));
+    *lse = (M + log2f(L.y)) * 0.6931471805599453f;
   }
 }
 
@@ -811,9 +838,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       tmem_st_wait();
       tc_fence_before();
       hand_over(&sm.m_next[w][r], -1, -INFINITY);
-      hand_over(&sm.l_sum[w][r], -1, 0.f);
+      hand_over(&sm.l_sum[w][r], -1, make_float2(0.f, 0.f));
       if (w == 0) {
-        hand_over(&sm.l_sum[2][r], -1, 0.f);
+        hand_over(&sm.l_sum[2][r], -1, make_float2(0.f, 0.f));
         sm.redo[r] = 0;
       }
       cp_async_wait<1>();
@@ -831,7 +858,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     const float sl2 = a.scale_log2;
     const int own_at = run_tiles + tiles_of(rank, sm.shared * kTile, a.log_c);      // the first own tile
     const int p_of = (run_tiles + w) & 1;      // the parity of this warpgroup's shared tiles
-    float M = -INFINITY, l = 0.f;      // -inf: not set yet
+    float M = -INFINITY;                 // -inf: not set yet
+    float2 l = make_float2(0.f, 0.f);
     bool first_known = false;
     int stage = w;                       // g % kStages
     for (int g = w;; g += 2, stage = stage + 2 >= kStages ? stage + 2 - kStages : stage + 2) {
@@ -892,10 +920,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       // P's buffer is free once the PV two tiles back has read it
       if (g >= 2 && !waitw(&sm.pv_done[w], (k - 1) & 1, a, abort_flag, 29)) break;
       tc_fence_after();
-      float sum = 0.f;
+      float2 sum = make_float2(0.f, 0.f);
       if (any) {
         const float negM = M == -INFINITY ? 0.f : -M;
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        float2 s0 = make_float2(0.f, 0.f), s1 = s0, e0 = s0, e1 = s0;
 #pragma unroll
         for (int cc = 0; cc < 128; cc += 32) {
           uint32_t pk[16];
@@ -906,39 +934,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
             const float x2 = ex2(fmaf(__uint_as_float(v[cc + e + 2]), sl2, negM));
             const float x3 = ex2(fmaf(__uint_as_float(v[cc + e + 3]), sl2, negM));
             const uint32_t p0 = pack_bf16(x0, x1), p1 = pack_bf16(x2, x3);
-            // (the weights that PV multiplies: numerator and denominator see one rounding)
-            s0 += __uint_as_float(p0 << 16);
-            s1 += __uint_as_float(p0 & 0xffff0000u);
-            s2 += __uint_as_float(p1 << 16);
-            s3 += __uint_as_float(p1 & 0xffff0000u);
+            add2(e0, x0, x1);
+            add2(e1, x2, x3);
+            // (the weights that PV multiplies)
+            add2(s0, __uint_as_float(p0 << 16), __uint_as_float(p0 & 0xffff0000u));
+            add2(s1, __uint_as_float(p1 << 16), __uint_as_float(p1 & 0xffff0000u));
             pk[e >> 1] = p0;
             pk[(e >> 1) + 1] = p1;
           }
           tmem_st16(pcol + (cc >> 1), pk);
         }
-        sum = mine ? (s0 + s1) + (s2 + s3) : 0.f;
+        if (mine) sum = make_float2((s0.x + s0.y) + (s1.x + s1.y), (e0.x + e0.y) + (e1.x + e1.y));
         tmem_st_wait();
       }
       tc_fence_before();
       mbar_arrive(&sm.p_full[w]);
-      if (sum > kMost) sm.redo[r] = 1;
+      if (sum.y > kMost) sm.redo[r] = 1;
       // Row sums: the runs' in their order, the entries' by parity (i / c) % 2.  Shared
       // tiles alternate between the warpgroups, so each has a parity of its own;
       // behind them a tile may come to either, and both go along.
       if (d.kind == kRuns) {
-        float run = 0.f;
+        float2 run = make_float2(0.f, 0.f);
         if (g > 0 && !take(&sm.l_sum[2][r], g - 1, &run, a, abort_flag, 35)) break;
         hand_over(&sm.l_sum[2][r], g, run + sum);
       } else if (d.kind == kShared) {
-        l += sum;
+        l = l + sum;
         hand_over(&sm.l_sum[p_of][r], g, l);
       } else {
-        float own = l, other = 0.f;
+        float2 own = l, other = make_float2(0.f, 0.f);
         if (g > run_tiles) {
           if (!take(&sm.l_sum[p_of ^ 1][r], g - 1, &other, a, abort_flag, 30)) break;
           if (g > own_at && !take(&sm.l_sum[p_of][r], g - 1, &own, a, abort_flag, 33)) break;
         }
-        if (d.at == p_of) own += sum; else other += sum;
+        if (d.at == p_of) own = own + sum; else other = other + sum;
         hand_over(&sm.l_sum[p_of ^ 1][r], g, other);
         hand_over(&sm.l_sum[p_of][r], g, own);
       }
@@ -956,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
     // (a row's M is set once: whichever parity has it, the other has it or nothing)
     const float m0 = handed(&sm.m_next[0][r], &t), m1 = handed(&sm.m_next[1][r], &t);
     const float M = m0 == -INFINITY ? m1 : m0;
-    const float l = (handed(&sm.l_sum[0][r], &t) + handed(&sm.l_sum[1][r], &t)) + handed(&sm.l_sum[2][r], &t);
+    const float2 l = (handed(&sm.l_sum[0][r], &t) + handed(&sm.l_sum[1][r], &t)) + handed(&sm.l_sum[2][r], &t);
     tc_fence_after();
     uint32_t x[64];
     const uint32_t ocol = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO + 64 * w;
@@ -1038,14 +1066,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   const int n_of = lane >> a.log_c, k_of = lane & (a.c - 1);
   const int r_of = row0 + warp + kWarps * n_of;
   const bool counts = finish && warp + kWarps * n_of < per && r_of < rows_all;
-  float mi = -INFINITY, li = 0.f;
+  float mi = -INFINITY;
+  float2 li = make_float2(0.f, 0.f);
   bool again = false;
   int h_of = 0;
   size_t row_of = 0;
   bool real = false;
   if (counts) {
     mi = ld_peer(peer_addr(&sm.m[r_of], k_of));
-    li = ld_peer(peer_addr(&sm.l[r_of], k_of));
+    li.x = ld_peer(peer_addr(&sm.l[r_of].x, k_of));
+    li.y = ld_peer(peer_addr(&sm.l[r_of].y, k_of));
     again = ld_peer_u8(peer_addr(&sm.redo[r_of], k_of)) != 0;
     const int u = static_cast<int>((static_cast<uint32_t>(r_of) * a.h_inv) >> 16);
     h_of = r_of - u * a.H;
@@ -1055,8 +1085,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
   float M = mi;
   for (int y = 1; y < a.c; y <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
   float fi = mi == -INFINITY ? 0.f : ex2(mi - M);
-  float L = fi * li;
-  for (int y = 1; y < a.c; y <<= 1) L += __shfl_xor_sync(0xffffffffu, L, y);
+  float2 L = make_float2(fi * li.x, fi * li.y);
+  for (int y = 1; y < a.c; y <<= 1) {
+    L.x += __shfl_xor_sync(0xffffffffu, L.x, y);
+    L.y += __shfl_xor_sync(0xffffffffu, L.y, y);
+  }
   float lse, sc;
   finish_row(M, L, sm.sink_l2[h_of], &sc, &lse);
   const uint32_t redo_lanes = __ballot_sync(0xffffffffu, real && again);
@@ -1145,9 +1178,9 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   a.ppt = 128 / a.H < kPairs ? 128 / a.H : kPairs;
   // Ranks for the longest sequence that the cache can hold, two entry tiles each at
   // least.  Few heads make few jobs, so up to eight ranks; many heads make a job
-  // a sequence, and four.  (47 x 2 queries of 16 heads, 19 tiles: 23.5 us with 4 ranks, 21.3
-  // with 8; 32 of 64 heads, 34 tiles: 22.5 us with 4, 35.3 with 8, whose clusters do not
-  // all fit at once.)
+  // a sequence, and four.  (47 x 2 queries of 16 heads, 19 tiles: 26.2 us with 4 ranks, 20.8
+  // with 8; 32 of 64 heads, 18 tiles: 19.4 us with 4, 31.1 with 8, whose clusters do not
+  // all fit at once; 4 of 64 heads, 34 tiles: 22.4 and 19.1.)
   const long long tiles = (static_cast<long long>(a.max_pages) * a.P + kTile - 1) / kTile;
   const int most_c = a.H > 32 && tiles < 128 ? 4 : 8;
   a.c = 1;
