@@ -14,7 +14,8 @@
 //   runs    8 runs of 16 keys, each of one pair: entries behind its last whole tile,
 //           then raw tokens of its window.
 // Own tiles and runs concern some rows only.  The PV MMA of such a tile writes
-// those rows' lanes alone (its lane mask), so a row's sum holds its own keys
+// those rows' lanes alone (its lane mask; a lone pair, whose lane 0 .. H - 1 count, needs
+// none: a masked MMA took 150 cycles more), so a row's sum holds its own keys
 // and nothing else: an infinity or NaN in one sequence's keys cannot reach
 // another's row as 0 * inf.  Keys a row must not see inside its own tiles are
 // zero-filled in shared memory and get P = 0.
@@ -77,16 +78,11 @@ struct Pair {
   int b, t, n, nw;        // sequence, token; visible entries; window rows (0 .. W)
   int p, slot;            // position, its ring slot
 };
-// A tile: its kind; own: the pairs u .. u + m - 1; runs: how many there are, the first's
-// number; an own tile's parity.  One 16-byte word.
+// A tile: its kind; own: the pairs u .. u + m - 1; at: an own tile's parity, the first
+// run's number.  One 16-byte word.
 struct __align__(16) Desc {
-  int kind, um, runs, at;
-  __device__ int u() const { return um & 0xff; }
-  __device__ int m() const { return um >> 8; }
+  int kind, u, m, at;
 };
-__device__ __forceinline__ Desc make_desc(int kind, int u, int m, int runs, int at) {
-  return Desc{kind, u | (m << 8), runs, at};
-}
 
 struct __align__(1024) Smem {
   uint8_t q[kTileBytes];
@@ -105,7 +101,6 @@ struct __align__(1024) Smem {
   Desc desc[kStages];
   float sink_l2[kTile];                // by head
   Pair pair[kPairs];
-  uint4 off[kPairs];                   // lanes that are not the pair's
   int npair;
   int group, tile, shared, leader;
   uint32_t tmem;
@@ -124,6 +119,7 @@ struct Args : PrefixAttnArgs {
   int ppt;              // pairs a job
   int tail_runs, win_runs;   // 16-key runs that a rank takes of each pair: entries, window
   int pair_runs, log_room;   // the room they have in the run tiles: a pair lies in one or fills several
+  uint4 off[kPairs];         // lanes that are not pair u's (here, a constant's address: an MMA takes them uniform)
   unsigned long long wait_ns;
   unsigned hint_ns;
 };
@@ -258,14 +254,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
                  "=r"((r)[27]), "=r"((r)[28]), "=r"((r)[29]), "=r"((r)[30]), "=r"((r)[31])                \
                : "r"(taddr))
 
-// D[tmem] += A[tmem] * B[smem]; lanes whose bit is set in `off` are not written.
-__device__ __forceinline__ void mma_ts_lanes(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             const uint4& off) {
+// If `on`, D[tmem] += A[tmem] * B[smem]; lanes whose bit is set in `off` are not written.
+__device__ __forceinline__ void mma_ts_lanes(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                             uint32_t idesc, const uint4& off) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, 1, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w)
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, 1, 0;\n\tsetp.ne.b32 q, %8, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w), "r"(on)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
@@ -299,12 +295,12 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // Bits of lanes outside [lo, hi), 32 at a time.
-__device__ __forceinline__ void lanes_off(uint32_t off[4], int lo, int hi) {
+__host__ __device__ __forceinline__ void lanes_off(uint32_t off[4], int lo, int hi) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int a = min(max(lo - 32 * i, 0), 32), b = min(max(hi - 32 * i, 0), 32);
-    const uint32_t below_b = b >= 32 ? 0xffffffffu : (1u << b) - 1u;
-    const uint32_t below_a = a >= 32 ? 0xffffffffu : (1u << a) - 1u;
+    const int a = lo - 32 * i, b = hi - 32 * i;
+    const uint32_t below_a = a >= 32 ? 0xffffffffu : a <= 0 ? 0u : (1u << a) - 1u;
+    const uint32_t below_b = b >= 32 ? 0xffffffffu : b <= 0 ? 0u : (1u << b) - 1u;
     off[i] = ~(below_b & ~below_a);
   }
 }
@@ -377,7 +373,8 @@ __device__ bool find_job(const Args& a, int job, Smem* sm, int* start, int* coun
   return false;
 }
 
-// Warp 0: the job's pairs, and the entries that all of them share (whole tiles).
+// Warp 0: the job's pairs, and the entries that all of them share (whole tiles): a lone
+// pair's all.
 __device__ void load_pairs(const Args& a, Smem& sm, int o0, int members) {
   const int lane = threadIdx.x & 31;
   const int first = sm.tile * a.ppt;
@@ -400,10 +397,9 @@ __device__ void load_pairs(const Args& a, Smem& sm, int o0, int members) {
       atomicCAS(a.status, 0, CSA_ERR_INVALID_ARG | (4 << 8));
     }
     sm.pair[lane] = pr;
-    uint32_t off[4];
-    lanes_off(off, lane * a.H, lane * a.H + a.H);
-    sm.off[lane] = make_uint4(off[0], off[1], off[2], off[3]);
-    n = min(n, pr.n);
+    n = np == 1 ? pr.n : min(n, pr.n);
+  } else if (np == 1) {
+    n = INT_MAX;
   } else if (lane == 31) {       // (a job has 16 pairs at most)
     n = lead < 0 || lead >= a.B
             ? 0
@@ -414,7 +410,7 @@ __device__ void load_pairs(const Args& a, Smem& sm, int o0, int members) {
   if (lane == 0) {
     sm.npair = np;
     sm.shared = n / kTile;
-    sm.leader = lead;
+    sm.leader = np == 1 ? a.group_seq[o0 + first / a.T] : lead;
   }
 }
 
@@ -655,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
               for (int k = 0; k < good; ++k, tile += a.c) {
                 if (use >= 1 && !wait1(&sm.kv_empty[stage], (use - 1) & 1, a, abort_flag, 20)) { fine = false; break; }
                 sm.valid[stage] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
-                sm.desc[stage] = make_desc(kind, u, m, 0, (tile >> a.log_c) & 1);
+                sm.desc[stage] = Desc{kind, u, m, (tile >> a.log_c) & 1};
                 mbar_expect_tx(&sm.kv_full[stage], kTileBytes);
                 uint32_t dst = smem_u32(sm.kv[stage]);
                 for (int x = 0; x < chunks; ++x, dst += a.box * 128) {
@@ -673,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
           }
           if (ok && good < batch) {
             const int key0 = i * kTile;
-            put(make_desc(kind, u, m, 0, (i >> a.log_c) & 1), kTile, [&](int r) { return pool_row(b, key0 + r); });
+            put(Desc{kind, u, m, (i >> a.log_c) & 1}, kTile, [&](int r) { return pool_row(b, key0 + r); });
             i += a.c;
           }
         }
@@ -687,12 +683,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         put_tiles(kOwn, u, m, sm.pair[u].b, own0, sm.pair[u].n / kTile);
         u += m;
       }
-      if (ok) put(make_desc(kEnd, 0, 0, 0, 0), 0, [](int) -> const void* { return nullptr; });
+      if (ok) put(Desc{kEnd, 0, 0, 0}, 0, [](int) -> const void* { return nullptr; });
       cp_async_wait<0>();
     } else {
       while (ok && g < run_tiles) {
         const int at = 8 * g, runs = min(8, sm.npair * room - at);
-        put(make_desc(kRuns, 0, 0, runs, at), runs * 16, [&](int r) -> const void* { return run_row(at + (r >> 4), r & 15); });
+        put(Desc{kRuns, 0, 0, at}, runs * 16, [&](int r) -> const void* { return run_row(at + (r >> 4), r & 15); });
       }
       cp_async_wait<0>();
     }
@@ -749,35 +745,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         if (d.kind == kEnd) break;
         const uint64_t kd = desc_mnmajor(smem_u32(sm.kv[stage]), 0);
         const uint32_t pcol = tmem + kColP + 64 * w;
+        // (steps without a key are left out: nothing was loaded for them)
+        const uint4 bits = sm.valid[stage];
+        const uint32_t words[4] = {bits.x, bits.y, bits.z, bits.w};
+        const bool whole = (bits.x & bits.y & bits.z & bits.w) == 0xffffffffu;
+        const bool all_rows = d.kind == kShared || sm.npair == 1;      // else the rows' lanes alone
         if (!wait1(&sm.p_full[w], (g >> 1) & 1, a, abort_flag, 26)) break;
         fence_proxy_async();
         tc_fence_after();
-        if (d.kind == kShared) {
+        if (all_rows && whole) {
 #pragma unroll
           for (int j = 0; j < kTile / 16; ++j) mma_ts(ocol, pcol + 8 * j, kd + j * (2048 >> 4), idesc_pv);
         } else {
-          // The rows' lanes alone; runs without a key are left out.
-          const bool own = d.kind == kOwn;
-          const uint4 bits = sm.valid[stage];
-          uint32_t todo = own ? 0xffu : (1u << d.runs) - 1u;
-          if (!(bits.x & 0xffffu)) todo &= ~1u;
-          if (!(bits.x >> 16)) todo &= ~2u;
-          if (!(bits.y & 0xffffu)) todo &= ~4u;
-          if (!(bits.y >> 16)) todo &= ~8u;
-          if (!(bits.z & 0xffffu)) todo &= ~16u;
-          if (!(bits.z >> 16)) todo &= ~32u;
-          if (!(bits.w & 0xffffu)) todo &= ~64u;
-          if (!(bits.w >> 16)) todo &= ~128u;
-          uint4 off = sm.off[own ? d.u() : 0];
-          for (int x = own ? d.u() + 1 : 0; own && x < d.u() + d.m(); ++x) {
-            const uint4 more = sm.off[x];
-            off = make_uint4(off.x & more.x, off.y & more.y, off.z & more.z, off.w & more.w);
-          }
-          while (todo) {
-            const int j = __ffs(todo) - 1;
-            todo &= todo - 1;
-            if (!own) off = sm.off[room <= 8 ? (d.at + j) >> a.log_room : d.at / room];
-            mma_ts_lanes(ocol, pcol + 8 * j, kd + j * (2048 >> 4), idesc_pv, off);
+          if (all_rows) {
+#pragma unroll
+            for (int j = 0; j < kTile / 16; ++j)
+              if (words[j >> 1] & (0xffffu << (16 * (j & 1)))) mma_ts(ocol, pcol + 8 * j, kd + j * (2048 >> 4), idesc_pv);
+          } else if (g < run_tiles) {
+#pragma unroll
+            for (int j = 0; j < kTile / 16; ++j)
+              mma_ts_lanes(words[j >> 1] & (0xffffu << (16 * (j & 1))), ocol, pcol + 8 * j, kd + j * (2048 >> 4), idesc_pv,
+                           a.off[room <= 8 ? (8 * g + j) >> a.log_room : 8 * g / room]);
+          } else {
+            uint4 off = a.off[d.u];
+            for (int u = d.u + 1; u < d.u + d.m; ++u) {
+              const uint4 more = a.off[u];
+              off = make_uint4(off.x & more.x, off.y & more.y, off.z & more.z, off.w & more.w);
+            }
+#pragma unroll
+            for (int j = 0; j < kTile / 16; ++j)
+              mma_ts_lanes(words[j >> 1] & (0xffffu << (16 * (j & 1))), ocol, pcol + 8 * j, kd + j * (2048 >> 4), idesc_pv,
+                           off);
           }
         }
         tc_commit(&sm.kv_empty[stage]);
@@ -835,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
         cp_async_mbar_arrive(&sm.kv_full[t]);
         if (lane == 0) {
           reinterpret_cast<uint16_t*>(&sm.valid[t])[warp] = static_cast<uint16_t>(word);
-          if (warp == 0) sm.desc[t] = make_desc(kRuns, 0, 0, min(8, sm.npair * room - 8 * t), 8 * t);
+          if (warp == 0) sm.desc[t] = Desc{kRuns, 0, 0, 8 * t};
           mbar_arrive(&sm.kv_full[t]);
         }
       }
@@ -888,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       bool mine = d.kind == kShared;       // the tile's MMA writes this row's lane
       int lo = 0, hi = kTile;
       if (d.kind == kOwn) {
-        mine = u >= d.u() && u < d.u() + d.m();
+        mine = u >= d.u && u < d.u + d.m;
       } else if (d.kind == kRuns) {
         lo = min(max(u * room - d.at, 0), 8) * 16;
         hi = min(max((u + 1) * room - d.at, 0), 8) * 16;
@@ -1216,6 +1214,11 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   CSA_REQUIRE(pairs < (1ll << 30), CSA_ERR_UNSUPPORTED);
   const long long jobs = pairs / a.ppt + a.G;       // at most: each group may leave one part full
   CSA_REQUIRE(jobs * a.c < (1ll << 31), CSA_ERR_UNSUPPORTED);
+  for (int u = 0; u < kPairs; ++u) {
+    uint32_t off[4];
+    lanes_off(off, u * a.H, u * a.H + a.H);
+    a.off[u] = make_uint4(off[0], off[1], off[2], off[3]);
+  }
   a.wait_ns = wait_limit_ns();
   a.hint_ns = static_cast<unsigned>(a.wait_ns < 200000ull ? a.wait_ns : 200000ull);
   const size_t smem = sizeof(Smem) + 1024;

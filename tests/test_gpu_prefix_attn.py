@@ -223,6 +223,22 @@ def test_bad_pages_are_skipped(mods, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_missing_shared_page_behind_nan(mods, dt):
+    """A page that all lack, late enough that its place was first filled with another
+    sequence's NaN."""
+    b = Batch([([0, 1], 1024)], [1030, 1040], 1, 16, 128, 128, 64, 128, dt, seed=12, max_pages=20)
+    b.ring[0] = float("nan")
+    b.table[:, 13] = -1
+    win = [j % b.cap for j in range(b.pos[1] - b.W + 1, b.pos[1] + 1)]
+    ent = b.pool[b.rows[1]].reshape(-1, b.D)[:b.n[1]]
+    keys = np64(torch.cat([ent[:13 * 64], ent[14 * 64:], b.ring[1, win]]))
+    out, lse = b.run(mods)
+    assert out[0].isnan().all()
+    b.keys = lambda i, t: keys
+    b.check(out, lse, seqs=[1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_logits_far_below_zero(mods, dt):
     """All of a row's logits near -300: parts of the split that see none of its keys
     do not set its scale."""
