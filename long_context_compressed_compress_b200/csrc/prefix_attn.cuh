@@ -26,9 +26,8 @@ struct PrefixAttnArgs {
 // Entries of sequence b that position p sees and the sequence's pages hold.
 __device__ __forceinline__ int visible_entries(const PrefixAttnArgs& a, int b, long long p) {
   if (p < 0) return 0;
-  const long long cap = static_cast<long long>(max(min(a.held[b], a.max_pages), 0)) * a.P;
-  const long long n = (p + 1) / a.m;
-  return static_cast<int>(n < cap ? n : cap);
+  const uint32_t cap = static_cast<uint32_t>(max(min(a.held[b], a.max_pages), 0)) * a.P;      // below 2^31
+  return static_cast<int>(min(static_cast<uint32_t>(p + 1) / static_cast<uint32_t>(a.m), cap));
 }
 
 int launch_prefix_attn_simt(const PrefixAttnArgs& a, int D, int dtype, cudaStream_t st);

@@ -107,6 +107,23 @@ def test_lists_longer_than_a_block(paged):
     same(c, m)
 
 
+@pytest.mark.parametrize("N", [8191, 8192, 8193, 20001])
+def test_caches_around_a_sweep(paged, N):
+    """Page counts around the 8192 that are gone through at once, nearly all of them
+    in use and then few, far apart."""
+    R = 9
+    c, m = pair(paged, L=1, N=N, P=1, D=8, R=R, max_entries=N)
+    both(c, m, "reserve", list(range(R)), [N // R] * R)
+    both(c, m, "free", [1, 4, 7])
+    both(c, m, "reserve", [4], [N // R + 100])
+    same(c, m)
+    both(c, m, "compact")
+    same(c, m)
+    both(c, m, "free", [0, 2, 3, 5, 6])
+    both(c, m, "compact")
+    same(c, m)
+
+
 BAD = [
     ("reserve", ([12], [4]), 1 | 1 << 8),                       # row out of range
     ("reserve", ([-1, 2], [4, 4]), 1 | 1 << 8),
