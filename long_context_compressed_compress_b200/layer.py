@@ -88,11 +88,11 @@ class NormRope:
         if kv_c.numel():
             ops.qk_norm_rope(None, kv_c, None, kv_c, zeros, kv_weight=self.entry_weight, pos_step=m, **self._kw())
 
-    def back(self, out, q_pos0):
+    def back(self, out, q_pos0, lens=None):
         """The attention's output, in place."""
         if self.derotate and self.inv_freq is not None:
             ops.qk_norm_rope(out, None, out, None, q_pos0, inv_freq=self.inv_freq, norm=False, inverse=True,
-                             interleaved=self.interleaved)
+                             interleaved=self.interleaved, lens=lens)
 
     @property
     def launches(self):
@@ -403,7 +403,7 @@ class HcaDecode:
         self.q_n = torch.empty_like(self.out) if norm_rope is not None else None
         self.groups = groups or paged.PrefixGroups.singles(R, device=device)
         self.launches = 4 + (norm_rope.launches - 2 if norm_rope is not None else 0)
-        self.graph = None
+        self.graph = self.captured = None
 
     def _append(self, a, z, lens=None):
         nr = self.norm_rope
@@ -443,7 +443,7 @@ class HcaDecode:
                                     self.ring, self.sink, c.tau, c.W, self.pos, self.out, c.m, lse=self.lse,
                                     status=self.cache.status)
         if self.norm_rope is not None:
-            self.norm_rope.back(self.out, self.pos)
+            self.norm_rope.back(self.out, self.pos, self.groups.attended)
         with t("csa_pos_advance"):
             ops.csa_pos_advance(self.pos, 1)
         return self.out
@@ -479,6 +479,7 @@ class HcaDecode:
                 self.step(x)
         torch.cuda.current_stream().wait_stream(s)
         self.graph = g
+        self.captured = (x, self.groups)       # (the graph reads them for as long as it lives)
         return g
 
     def replay(self):

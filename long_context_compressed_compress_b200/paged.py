@@ -32,6 +32,11 @@ class PrefixGroups:
         self.B, self.G, self.n_seq = int(B), len(shared), len(seq)
         self.off, self.seq, self.shared = (torch.tensor(v or [0], dtype=torch.int32).to(device)
                                            for v in (off, seq, shared))
+        # int32 [B], 1 for a sequence of some group; None where all are
+        self.attended = None
+        if self.n_seq < self.B:
+            listed = set(seq)
+            self.attended = torch.tensor([int(b in listed) for b in range(self.B)], dtype=torch.int32).to(device)
         # what a call passes on (this object owns the tensors behind the pointers)
         self.dev = self.off.get_device()
         self.off_ptr, self.seq_ptr, self.shared_ptr = (t.data_ptr() for t in (self.off, self.seq, self.shared))

@@ -204,3 +204,30 @@ def test_csa_prefill_with_norm_and_rotation(mods):
     torch.cuda.synchronize()
     assert torch.equal(got, out)
     assert not torch.equal(got, b.out)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_idle_rows_keep_their_outputs(mods, dt):
+    """Rows that no group lists keep the output of their last step, rotation and all; a
+    captured step goes on with the groups it was captured with."""
+    layer, paged = mods
+    cfg = configs._hca(B=4, T=256, H=8, D=128, m=16, W=40, dtype=dt, tau=0.1)
+    cache = paged.PagedEntries(1, 40, 4, cfg.D, cfg.B, cfg.S, dtype=torch.bfloat16 if dt == "bf16" else torch.float32)
+    ropes = layer.NormRope(**{k: v.cuda() for k, v in rope(cfg.D, 32, 3).items()})
+    dec = layer.HcaDecode(cfg, cache, norm_rope=ropes)
+    cache.reserve([0, 1, 2, 3], [cfg.S] * 4)
+    x = drawn(cfg, 4, 50, 5)
+    dec.load({k: v.cuda() for k, v in x.items() if k != "q"})
+    static = {k: v[:, 0].contiguous().cuda() for k, v in drawn(cfg, 4, 1, 6).items()}
+    first = dec.step(static).clone()
+    dec.groups = paged.PrefixGroups([([2], 0), ([0], 0)], 4)
+    second = dec.step(static).clone()
+    assert torch.equal(second[[1, 3]], first[[1, 3]])
+    assert not torch.equal(second[[0, 2]], first[[0, 2]])
+    dec.capture(static)
+    dec.groups = paged.PrefixGroups.singles(4)
+    third = dec.replay().clone()
+    torch.cuda.synchronize()
+    assert cache.status.item() == 0
+    assert torch.equal(third[[1, 3]], first[[1, 3]])
+    assert not torch.equal(third[[0, 2]], second[[0, 2]])
