@@ -470,7 +470,7 @@ int hca_paged_append(const void* a, const void* z, int dtype, int B, int T,
  *     member lists; n_seq = group_off[G].  Sequences that no group lists are
  *     left as they were.
  * A query that sees nothing (or only a sink) gives 0 and lse = -inf.
- * Deterministic: a row's result depends on the row, its keys and
+ * Deterministic: a row's result depends on the row, its keys, H, W and
  * max_pages * P, not on the batch, the grouping or T.
  * bf16 with D = 128 and H <= 128 runs on tcgen05, the rest on CUDA cores
  * (H <= 1024).  Requires D in {64, 128}, P >= 1, 16-byte aligned tensors.
