@@ -353,7 +353,7 @@ __device__ bool find_job(const Args& a, int job, Smem* sm, int* start, int* coun
     if (g < a.G) {
       o0 = group_start(a, g);
       n = max(group_start(a, g + 1) - o0, 0);
-      jobs = static_cast<int>((static_cast<long long>(n) * a.T + a.ppt - 1) / a.ppt);
+      jobs = static_cast<int>((static_cast<uint32_t>(n) * a.T + a.ppt - 1) / static_cast<uint32_t>(a.ppt));
     }
     const int incl = warp_incl_scan(jobs);
     const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > job);
