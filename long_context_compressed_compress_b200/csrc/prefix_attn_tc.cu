@@ -627,6 +627,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       const int x = entry_row(a, b, key);
       return x >= 0 ? static_cast<const __nv_bfloat16*>(a.pool) + static_cast<size_t>(x) * kDim : nullptr;
     };
+    // The further run tiles: the odd or the even ones.
+    auto put_runs = [&](int odd) {
+      while (ok && g < run_tiles) {
+        if ((g & 1) != odd) {
+          ok = stage_free();
+          ++g;
+          continue;
+        }
+        const int at = 8 * g, runs = min(8, sm.npair * room - at);
+        put(Desc{kRuns, 0, 0, at}, runs * 16, [&](int r) -> const void* { return run_row(at + (r >> 4), r & 15); });
+      }
+    };
     if (warp == kEntryWarp) {
       // This rank's entry tiles i, i + c, .. of sequence b below tile `end`.  The page chunks of
       // the next 32 / chunks tiles are looked up at once, a lane each; then one
@@ -674,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
           }
         }
       };
-      for (; ok && g < run_tiles; ++g) ok = stage_free();
+      put_runs(1);
       g = run_tiles;
       put_tiles(kShared, 0, 0, sm.leader, rank, sm.shared);
       for (int u = 0; u < sm.npair && ok;) {
@@ -686,10 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(const __grid_c
       if (ok) put(Desc{kEnd, 0, 0, 0}, 0, [](int) -> const void* { return nullptr; });
       cp_async_wait<0>();
     } else {
-      while (ok && g < run_tiles) {
-        const int at = 8 * g, runs = min(8, sm.npair * room - at);
-        put(Desc{kRuns, 0, 0, at}, runs * 16, [&](int r) -> const void* { return run_row(at + (r >> 4), r & 15); });
-      }
+      put_runs(0);
       cp_async_wait<0>();
     }
   } else if (!idle && warp == kQkWarp) {
@@ -1185,7 +1194,6 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   if (a.box && !make_pool_map(&map, a.pool, static_cast<uint64_t>(a.N) * a.P, a.box)) return CSA_ERR_CUDA;
   CSA_REQUIRE(static_cast<long long>(a.N) * a.P < (1ll << 31), CSA_ERR_UNSUPPORTED);
   CSA_REQUIRE(a.W == 0 || static_cast<long long>(a.B) * a.raw_cap < (1ll << 31) - 2, CSA_ERR_UNSUPPORTED);
-  a.ppt = 128 / a.H < kPairs ? 128 / a.H : kPairs;
   // Ranks for the longest sequence that the cache can hold, two entry tiles each at
   // least.  Few heads make few jobs, so up to eight ranks; many heads make a job
   // a sequence, and four.  (47 x 2 queries of 16 heads, 19 tiles: 26.2 us with 4 ranks, 20.8
@@ -1200,7 +1208,8 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   // above P, ceil(2^(31 + s) / P) fits 32 bits and errs by less than 2^s.
   a.p_shift = a.P > 1 ? 31 - __builtin_clz(static_cast<unsigned>(a.P - 1)) : 0;      // s - 1
   a.p_mul = a.P > 1 ? static_cast<uint32_t>(((1ull << (32 + a.p_shift)) + a.P - 1) / a.P) : 0;
-  a.tail_runs = 8 / a.c;
+  // (of a cache that cannot fill a tile only the runs that it can)
+  a.tail_runs = static_cast<int>(min(8ll / a.c, (static_cast<long long>(a.max_pages) * a.P + 15) / 16));
   a.win_runs = ((a.W + 15) / 16 + a.c - 1) / a.c;
   // room for them: a power of two below 8 or a multiple of it, so that a pair's runs do
   // not straddle a tile's end (its first tile sets its rows' stabiliser)
@@ -1212,8 +1221,6 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   cudaGetDevice(&dev);
   const long long pairs = static_cast<long long>(a.n_seq) * a.T;
   CSA_REQUIRE(pairs < (1ll << 30), CSA_ERR_UNSUPPORTED);
-  const long long jobs = pairs / a.ppt + a.G;       // at most: each group may leave one part full
-  CSA_REQUIRE(jobs * a.c < (1ll << 31), CSA_ERR_UNSUPPORTED);
   for (int u = 0; u < kPairs; ++u) {
     uint32_t off[4];
     lanes_off(off, u * a.H, u * a.H + a.H);
@@ -1223,15 +1230,8 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   a.hint_ns = static_cast<unsigned>(a.wait_ns < 200000ull ? a.wait_ns : 200000ull);
   const size_t smem = sizeof(Smem) + 1024;
   const auto kernel = a.lse ? prefix_attn_kernel<true> : prefix_attn_kernel<false>;
-  static bool attr_set[2][64] = {};
-  bool* const set = dev < 0 || dev >= 64 ? nullptr : &attr_set[a.lse != nullptr][dev];
-  if (!set || !*set) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return set_cuda_error(e);
-    if (set) *set = true;
-  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(jobs * a.c));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.c));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -1242,7 +1242,38 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, map);
+  // Set once per device: the kernel's shared memory; how many clusters run at once.
+  static bool attr_set[2][64] = {};
+  static int at_once[64][4] = {};
+  const bool known = dev >= 0 && dev < 64;
+  cudaError_t e;
+  if (!known || !attr_set[a.lse != nullptr][dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return set_cuda_error(e);
+    if (known) attr_set[a.lse != nullptr][dev] = true;
+  }
+  int slots = known ? at_once[dev][a.log_c] : 0;
+  if (slots == 0) {
+    e = cudaOccupancyMaxActiveClusters(&slots, kernel, &cfg);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    slots = slots > 1 ? slots : 1;
+    if (known) at_once[dev][a.log_c] = slots;
+  }
+  // Pairs a job: few, so that the jobs fill the SMs, but no more jobs than run at once, up to
+  // what its rows and the set-up allow.  (A row's bits are the same in any job.  With the
+  // most at all times 12 x 4 queries of 8 heads over 46 entries took 75 us for 9.2, 64
+  // of 16 heads 37 for 11.0; with jobs for 148 SMs in clusters of eight, of which SLOTS run
+  // at once, 47 x 2 queries of 16 heads in three groups 31.5 us for FIGURE.)
+  const int most = 128 / a.H < kPairs ? 128 / a.H : kPairs;
+  a.ppt = 1;
+  if (pairs > slots) {
+    const long long full = slots - a.G;         // (each group may leave one job part full)
+    a.ppt = full > 0 && (pairs + full - 1) / full < most ? static_cast<int>((pairs + full - 1) / full) : most;
+  }
+  const long long jobs = min(pairs, pairs / a.ppt + a.G);
+  CSA_REQUIRE(jobs * a.c < (1ll << 31), CSA_ERR_UNSUPPORTED);
+  cfg.gridDim = dim3(static_cast<unsigned>(jobs * a.c));
+  e = cudaLaunchKernelEx(&cfg, kernel, a, map);
   if (e != cudaSuccess) return set_cuda_error(e);
   return check_launch();
 }
