@@ -10,6 +10,8 @@
 // the rows four at a time with all loads under way.  (A CTA-wide table of
 // angles in shared memory cost a barrier and half the occupancy: 355 to 646 us for
 // 32768 tokens of 64 heads.)
+#include <type_traits>
+
 #include "rope.cuh"
 
 namespace csa {
@@ -110,6 +112,56 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T_) == 2 && !HALF ? 4 : 3) 
   }
 }
 
+// Tokens of no more rows than a warp holds (the key alone, one head and the key): a warp
+// takes TOK tokens, RW / TOK rows of each, and a token's lanes form its angles, which
+// bound such calls.  (293184 tokens of a head and a key, D = 64: 77 us, 203 by the kernel
+// above with a token a warp; loads ahead for a warp's next tokens: 83.)
+template <typename T_, int D, bool HALF, int TOK>
+__global__ void __launch_bounds__(kNrThreads, 4) norm_rope_few_kernel(const NormRopeArgs a) {
+  constexpr int G = D / 8, RW = 32 / G, RP = RW / TOK;
+  const int lane = threadIdx.x & 31, l = lane % G, r = lane / G % RP;
+  const uint32_t item = blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
+  if (item * TOK >= a.items) return;
+  const uint32_t tok = min(item * TOK + lane / (G * RP), a.items - 1);
+  const bool own = item * TOK + lane / (G * RP) < a.items;
+  const uint32_t b = tok / static_cast<uint32_t>(a.T);
+  const int t = static_cast<int>(tok - b * a.T), len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+  const bool live = own && t < len && r < a.rows, is_q = r < a.H;
+  const long long j = static_cast<long long>(a.pos0[b]) + t;
+  const T_* s = (is_q ? static_cast<const T_*>(a.q) + b * a.q_bs + t * a.q_ts + r * D
+                      : static_cast<const T_*>(a.kv) + b * a.kv_bs + t * a.kv_ts) + l * 8;
+  T_* d = nullptr;
+  if (is_q) {
+    d = static_cast<T_*>(a.q_out) + (static_cast<long long>(tok) * a.H + r) * D + l * 8;
+  } else if (a.kv_inplace) {
+    d = static_cast<T_*>(a.kv_out) + static_cast<long long>(tok) * D + l * 8;
+  } else if (t >= len - a.kv_cap) {
+    long long slot = j >= 0 && j < (1ll << 31) ? static_cast<uint32_t>(j) % static_cast<uint32_t>(a.kv_cap) : j % a.kv_cap;
+    if (slot < 0) slot += a.kv_cap;
+    d = static_cast<T_*>(a.kv_out) + (static_cast<long long>(b) * a.kv_cap + slot) * D + l * 8;
+  }
+  Raw8<T_> raw;
+  if (live) raw.load(s);
+  else raw.zero();
+  LaneRope lr;
+  if (a.R > 0) lane_rope<D, HALF, 32 / TOK>(lr, j * a.pos_step, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
+  else lr.active = lr.second = false;
+  float v[8];
+  raw.get(v);
+  if (a.flags & CSA_NORM) {
+    const float* w = is_q ? a.q_w : a.kv_w;
+    const float sc = row_rms_scale<D>(v, a.eps);
+    float w8[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w8[e] = 1.f;
+    if (w) Vec8<float>::load(w + l * 8, w8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= sc * w8[e];
+  }
+  rotate8<HALF>(v, lr, a.R);
+  if (live && d) Vec8<T_>::store(d, v);
+}
+
 // [lo, hi) bytes of a strided tensor
 struct Span {
   uintptr_t lo, hi;
@@ -126,6 +178,18 @@ int launch_norm_rope(NormRopeArgs& a, cudaStream_t st) {
   // small part of it, but short where there are few rows, to spread them over the SMs.
   constexpr int RW = 32 / (D / 8);
   const long long tokens = a.items;
+  if (a.rows <= RW) {
+    const auto few = [&](auto tok) {
+      constexpr int TOK = decltype(tok)::value;
+      const uint32_t warps = (a.items + TOK - 1) / TOK, grid = (warps + kNrThreads / 32 - 1) / (kNrThreads / 32);
+      if (a.flags & CSA_ROPE_HALF) norm_rope_few_kernel<T_, D, true, TOK><<<grid, kNrThreads, 0, st>>>(a);
+      else norm_rope_few_kernel<T_, D, false, TOK><<<grid, kNrThreads, 0, st>>>(a);
+      return check_launch();
+    };
+    if (a.rows == 1) return few(std::integral_constant<int, RW>());
+    if (RW == 4 && a.rows == 2) return few(std::integral_constant<int, RW == 4 ? 2 : 1>());
+    return few(std::integral_constant<int, 1>());
+  }
   int iters = 16;
   while (iters > 1 && tokens * ((a.rows + iters * RW - 1) / (iters * RW)) < 148 * 32) iters /= 2;
   a.chunk = iters * RW;

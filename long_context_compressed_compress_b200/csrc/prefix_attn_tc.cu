@@ -1196,9 +1196,9 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   CSA_REQUIRE(a.W == 0 || static_cast<long long>(a.B) * a.raw_cap < (1ll << 31) - 2, CSA_ERR_UNSUPPORTED);
   // Ranks for the longest sequence that the cache can hold, two entry tiles each at
   // least.  Few heads make few jobs, so up to eight ranks; many heads make a job
-  // a sequence, and four.  (47 x 2 queries of 16 heads, 19 tiles: 26.2 us with 4 ranks, 20.8
-  // with 8; 32 of 64 heads, 18 tiles: 19.4 us with 4, 31.1 with 8, whose clusters do not
-  // all fit at once; 4 of 64 heads, 34 tiles: 22.4 and 19.1.)
+  // a sequence, and four.  (32 of 16 heads, 66 tiles: 28.3 us with 4 ranks, 21.6 with 8; 32
+  // of 64 heads, 18 tiles: 18.2 us with 4, 31.5 with 8, whose clusters do not all run at
+  // once; 4 of 64 heads, 34 tiles: 20.0 and 17.0.)
   const long long tiles = (static_cast<long long>(a.max_pages) * a.P + kTile - 1) / kTile;
   const int most_c = a.H > 32 && tiles < 128 ? 4 : 8;
   a.c = 1;
@@ -1262,8 +1262,8 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   // Pairs a job: few, so that the jobs fill the SMs, but no more jobs than run at once, up to
   // what its rows and the set-up allow.  (A row's bits are the same in any job.  With the
   // most at all times 12 x 4 queries of 8 heads over 46 entries took 75 us for 9.2, 64
-  // of 16 heads 37 for 11.0; with jobs for 148 SMs in clusters of eight, of which SLOTS run
-  // at once, 47 x 2 queries of 16 heads in three groups 31.5 us for FIGURE.)
+  // of 16 heads 37 for 11.0; with jobs for 148 SMs in clusters of eight, of which 15 run
+  // at once, 47 x 2 queries of 16 heads in three groups 31.5 us for 20.4.)
   const int most = 128 / a.H < kPairs ? 128 / a.H : kPairs;
   a.ppt = 1;
   if (pairs > slots) {

@@ -2,7 +2,7 @@
 
 Tolerances.  fp32 error of one output, relative to |y0| + |y1| of its rotated
 pair: the sum of squares adds 8 terms a lane and up to 5 shuffle steps (13 half
-steps, halved by the root), the root 2, the two products 2, cos and sin 2 each,
+steps, halved by the root), the root 2, the two products 2, cos and sin 3 each,
 the rotation's two roundings: below 24 half steps of 2^-24.  The stored value
 then rounds by half a step of its type."""
 import numpy as np
@@ -166,3 +166,42 @@ def test_nan_and_zero_rows_stay_in_their_rows(ops):
     keep = torch.ones(T, H, dtype=torch.bool)
     keep[1, 2] = False
     assert out[0][keep.cuda()].isfinite().all()
+
+
+@pytest.mark.parametrize("R", [0, 16, "D"])
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,H,kv", [(64, 0, 1), (64, 1, 1), (64, 1, 0), (64, 2, 0), (128, 0, 1), (128, 1, 0)])
+def test_few_rows_a_token(ops, D, H, kv, dt, inter, R):
+    """Tokens of one or two rows, several of them in a warp: an odd number, some behind
+    their row's length, a ring shorter than the call."""
+    B, T, cap = 3, 7, 5
+    R = D if R == "D" else R
+    lens, pos = [7, 0, 6], [1 << 20, 4, 250]
+    g = torch.Generator().manual_seed(D + H)
+    q = torch.randn(B, T, H, D, generator=g).to(DT[dt]) if H else None
+    k = torch.randn(B, T, D, generator=g).to(DT[dt]) if kv else None
+    qw, kw = torch.randn(D, generator=g), torch.randn(D, generator=g)
+    qo = torch.full((B, T, H, D), 7.0, dtype=DT[dt]).cuda() if H else None
+    ring = torch.full((B, cap, D), 7.0, dtype=DT[dt]).cuda() if kv else None
+    f = freq(R)
+    ops.qk_norm_rope(None if q is None else q.cuda(), None if k is None else k.cuda(), qo, ring,
+                     torch.tensor(pos, dtype=torch.int32).cuda(), q_weight=qw.cuda(), kv_weight=kw.cuda(),
+                     inv_freq=None if f is None else torch.tensor(f).cuda(), interleaved=inter,
+                     lens=torch.tensor(lens, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    for b in range(B):
+        j, n = pos[b] + np.arange(T), lens[b]
+        if H:
+            y = serving.norm_rope(np64(q[b]), 0, None, np64(qw))
+            close(np64(qo[b, :n]), serving.norm_rope(np64(q[b]), j[:, None], f, np64(qw), interleaved=inter)[:n], y[:n],
+                  R, inter, dt)
+            assert (np64(qo[b, n:]) == 7.0).all()
+        if kv:
+            y = serving.norm_rope(np64(k[b]), 0, None, np64(kw))
+            ref = serving.norm_rope(np64(k[b]), j, f, np64(kw), interleaved=inter)
+            live = range(max(0, n - cap), n)
+            for t in live:
+                close(np64(ring[b, j[t] % cap]), ref[t], y[t], R, inter, dt)
+            other = sorted(set(range(cap)) - {int(j[t] % cap) for t in live})
+            assert (np64(ring[b, other]) == 7.0).all()
