@@ -1194,15 +1194,19 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   if (a.box && !make_pool_map(&map, a.pool, static_cast<uint64_t>(a.N) * a.P, a.box)) return CSA_ERR_CUDA;
   CSA_REQUIRE(static_cast<long long>(a.N) * a.P < (1ll << 31), CSA_ERR_UNSUPPORTED);
   CSA_REQUIRE(a.W == 0 || static_cast<long long>(a.B) * a.raw_cap < (1ll << 31) - 2, CSA_ERR_UNSUPPORTED);
-  // Ranks for the longest sequence that the cache can hold, two entry tiles each at
-  // least.  Few heads make few jobs, so up to eight ranks; many heads make a job
+  // Ranks for the longest sequence that the cache can hold, three entry tiles each at
+  // least: a tile takes a microsecond, a CTA's set-up and join ten.  (8 tiles of 64 heads: a
+  // sequence alone 14.1 us with 4 ranks, 15.6 with 2; 100 of them, which then run at
+  // once, 31.7 and 19.1.  4 tiles of 128 heads, 1 and 100: 14.5 and 30.0 us with 2,
+  // 13.9 and 15.2 with one.)
+  // Few heads make few jobs, so up to eight ranks; many heads make a job
   // a sequence, and four.  (32 of 16 heads, 66 tiles: 28.3 us with 4 ranks, 21.6 with 8; 32
   // of 64 heads, 18 tiles: 18.2 us with 4, 31.5 with 8, whose clusters do not all run at
   // once; 4 of 64 heads, 34 tiles: 20.0 and 17.0.)
   const long long tiles = (static_cast<long long>(a.max_pages) * a.P + kTile - 1) / kTile;
   const int most_c = a.H > 32 && tiles < 128 ? 4 : 8;
   a.c = 1;
-  while (a.c < most_c && 4 * a.c <= tiles) a.c *= 2;
+  while (a.c < most_c && 6 * a.c <= tiles) a.c *= 2;
   a.log_c = 31 - __builtin_clz(static_cast<unsigned>(a.c));
   // The round-up reciprocal of P for 31-bit numerators: with 2^s the power of two at or
   // above P, ceil(2^(31 + s) / P) fits 32 bits and errs by less than 2^s.
