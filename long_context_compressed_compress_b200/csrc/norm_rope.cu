@@ -39,7 +39,7 @@ constexpr int kNrThreads = 256;
 constexpr int kFlight = 4;
 
 template <typename T_, int D, bool HALF>
-__global__ void __launch_bounds__(kNrThreads, sizeof(T_) == 2 && !HALF ? 4 : 3) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrThreads, sizeof(T_) == 2 ? 4 : 3) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int G = D / 8, RW = 32 / G;       // lanes a row, rows a warp
   const int lane = threadIdx.x & 31, l = lane % G, sub = lane / G;
   const uint32_t item = blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
@@ -51,36 +51,36 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T_) == 2 && !HALF ? 4 : 3) 
   const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
   if (t >= len) return;
   const long long j = static_cast<long long>(a.pos0[b]) + t;
-  const T_* qs = static_cast<const T_*>(a.q) + b * a.q_bs + t * a.q_ts + l * 8;
-  T_* qd = static_cast<T_*>(a.q_out) + tok * a.H * D + l * 8;
-  const T_* ks = static_cast<const T_*>(a.kv) + b * a.kv_bs + t * a.kv_ts + l * 8;
+  const LaneRuns at = lane_runs<D>(l, a.R, HALF);
+  const int apart = at.b - at.a;
+  const T_* qs = static_cast<const T_*>(a.q) + b * a.q_bs + t * a.q_ts + at.a;
+  T_* qd = static_cast<T_*>(a.q_out) + tok * a.H * D + at.a;
+  const T_* ks = static_cast<const T_*>(a.kv) + b * a.kv_bs + t * a.kv_ts + at.a;
   T_* kd = nullptr;                           // of the call's tokens only the last kv_cap reach the ring
   if (a.kv_inplace) {
-    kd = static_cast<T_*>(a.kv_out) + tok * D + l * 8;
+    kd = static_cast<T_*>(a.kv_out) + tok * D + at.a;
   } else if (a.kv_out && t >= len - a.kv_cap) {
     long long slot = j >= 0 && j < (1ll << 31) ? static_cast<uint32_t>(j) % static_cast<uint32_t>(a.kv_cap) : j % a.kv_cap;
     if (slot < 0) slot += a.kv_cap;
-    kd = static_cast<T_*>(a.kv_out) + (static_cast<long long>(b) * a.kv_cap + slot) * D + l * 8;
+    kd = static_cast<T_*>(a.kv_out) + (static_cast<long long>(b) * a.kv_cap + slot) * D + at.a;
   }
 
-  Raw8<T_> raw[kFlight];
+  Raw8<T_, HALF> raw[kFlight];
   auto fetch = [&](int base) {
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
       const int r = base + i * RW + sub;
-      if (r < r1) raw[i].load(r < a.H ? qs + static_cast<long long>(r) * D : ks);
+      if (r < r1) raw[i].load(r < a.H ? qs + static_cast<long long>(r) * D : ks, apart);
       else raw[i].zero();
     }
   };
   fetch(r0);
   LaneRope lr;
-  if (a.R > 0) lane_rope<D, HALF>(lr, j * a.pos_step, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
-  else lr.active = lr.second = false;
+  if (a.R > 0) lane_rope<D>(lr, j * a.pos_step, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
+  else lr.active = false;
   const bool norm = a.flags & CSA_NORM;
   float w[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = 1.f;
-  if (norm && a.q_w) Vec8<float>::load(a.q_w + l * 8, w);
+  weights8(norm ? a.q_w : nullptr, at, w);
   for (int base = r0; base < r1; base += kFlight * RW) {
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
@@ -95,17 +95,15 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T_) == 2 && !HALF ? 4 : 3) 
           for (int e = 0; e < 8; ++e) v[e] *= sc * w[e];
         } else {
           float kw[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) kw[e] = 1.f;
-          if (a.kv_w) Vec8<float>::load(a.kv_w + l * 8, kw);
+          weights8(a.kv_w, at, kw);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] *= sc * kw[e];
         }
       }
-      rotate8<HALF>(v, lr, a.R);
+      rotate8<HALF>(v, lr);
       if (r < r1) {
         T_* d = r < a.H ? qd + static_cast<long long>(r) * D : kd;
-        if (d) Vec8<T_>::store(d, v);
+        if (d) store8<HALF>(d, apart, v);
       }
     }
     if (base + kFlight * RW < r1) fetch(base + kFlight * RW);
@@ -114,8 +112,8 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T_) == 2 && !HALF ? 4 : 3) 
 
 // Tokens of no more rows than a warp holds (the key alone, one head and the key): a warp
 // takes TOK tokens, RW / TOK rows of each, and a token's lanes form its angles, which
-// bound such calls.  (293184 tokens of a head and a key, D = 64: 77 us, 203 by the kernel
-// above with a token a warp; loads ahead for a warp's next tokens: 83.)
+// bound such calls.  (293184 tokens of a head and a key, D = 64, split halves: 58 us, 203
+// with a token a warp.)
 template <typename T_, int D, bool HALF, int TOK>
 __global__ void __launch_bounds__(kNrThreads, 4) norm_rope_few_kernel(const NormRopeArgs a) {
   constexpr int G = D / 8, RW = 32 / G, RP = RW / TOK;
@@ -126,40 +124,39 @@ __global__ void __launch_bounds__(kNrThreads, 4) norm_rope_few_kernel(const Norm
   const bool own = item * TOK + lane / (G * RP) < a.items;
   const uint32_t b = tok / static_cast<uint32_t>(a.T);
   const int t = static_cast<int>(tok - b * a.T), len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+  const LaneRuns at = lane_runs<D>(l, a.R, HALF);
+  const int apart = at.b - at.a;
   const bool live = own && t < len && r < a.rows, is_q = r < a.H;
   const long long j = static_cast<long long>(a.pos0[b]) + t;
   const T_* s = (is_q ? static_cast<const T_*>(a.q) + b * a.q_bs + t * a.q_ts + r * D
-                      : static_cast<const T_*>(a.kv) + b * a.kv_bs + t * a.kv_ts) + l * 8;
+                      : static_cast<const T_*>(a.kv) + b * a.kv_bs + t * a.kv_ts) + at.a;
   T_* d = nullptr;
   if (is_q) {
-    d = static_cast<T_*>(a.q_out) + (static_cast<long long>(tok) * a.H + r) * D + l * 8;
+    d = static_cast<T_*>(a.q_out) + (static_cast<long long>(tok) * a.H + r) * D + at.a;
   } else if (a.kv_inplace) {
-    d = static_cast<T_*>(a.kv_out) + static_cast<long long>(tok) * D + l * 8;
+    d = static_cast<T_*>(a.kv_out) + static_cast<long long>(tok) * D + at.a;
   } else if (t >= len - a.kv_cap) {
     long long slot = j >= 0 && j < (1ll << 31) ? static_cast<uint32_t>(j) % static_cast<uint32_t>(a.kv_cap) : j % a.kv_cap;
     if (slot < 0) slot += a.kv_cap;
-    d = static_cast<T_*>(a.kv_out) + (static_cast<long long>(b) * a.kv_cap + slot) * D + l * 8;
+    d = static_cast<T_*>(a.kv_out) + (static_cast<long long>(b) * a.kv_cap + slot) * D + at.a;
   }
-  Raw8<T_> raw;
-  if (live) raw.load(s);
+  Raw8<T_, HALF> raw;
+  if (live) raw.load(s, apart);
   else raw.zero();
   LaneRope lr;
-  if (a.R > 0) lane_rope<D, HALF, 32 / TOK>(lr, j * a.pos_step, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
-  else lr.active = lr.second = false;
+  if (a.R > 0) lane_rope<D, 32 / TOK>(lr, j * a.pos_step, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
+  else lr.active = false;
   float v[8];
   raw.get(v);
   if (a.flags & CSA_NORM) {
-    const float* w = is_q ? a.q_w : a.kv_w;
     const float sc = row_rms_scale<D>(v, a.eps);
     float w8[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w8[e] = 1.f;
-    if (w) Vec8<float>::load(w + l * 8, w8);
+    weights8(is_q ? a.q_w : a.kv_w, at, w8);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= sc * w8[e];
   }
-  rotate8<HALF>(v, lr, a.R);
-  if (live && d) Vec8<T_>::store(d, v);
+  rotate8<HALF>(v, lr);
+  if (live && d) store8<HALF>(d, apart, v);
 }
 
 // [lo, hi) bytes of a strided tensor

@@ -277,39 +277,33 @@ __global__ void __launch_bounds__(kSlots * D / 4, kSmThreads / (kSlots * D / 4))
     __syncthreads();
     // row k of lanes finishes entry k (whole warps take part: rows behind the last are zeros)
     if (threadIdx.x < (E * G + 31) / 32 * 32) {
+      const bool half = a.flags & CSA_ROPE_HALF;
+      const LaneRuns own = lane_runs<D>(l, a.R, half);
+      Raw8<float, true> raw;
       float v[8];
-      if (row < nblk) {
-        Vec8<float>::load(&entry[row][l * 8], v);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = 0.f;
-      }
+      if (row < nblk) raw.load(&entry[row][own.a], own.b - own.a);
+      else raw.zero();
+      raw.get(v);
       if (a.flags & CSA_NORM) {
         const float sc = row_rms_scale<D>(v, a.eps);
         float w[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = 1.f;
-        if (a.weight) Vec8<float>::load(a.weight + l * 8, w);
+        weights8(a.weight, own, w);
 #pragma unroll
         for (int c = 0; c < 8; ++c) v[c] *= sc * w[c];
       }
       if (a.R > 0) {
         LaneRope lr;
         const long long at = static_cast<long long>(first + blk0 + min(row, nblk - 1)) * a.m;
-        if (a.flags & CSA_ROPE_HALF) {
-          lane_rope_alone<D, true>(lr, at, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
-          rotate8<true>(v, lr, a.R);
-        } else {
-          lane_rope_alone<D, false>(lr, at, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
-          rotate8<false>(v, lr, a.R);
-        }
+        lane_rope_alone<D>(lr, at, a.inv_freq, a.R, a.flags & CSA_ROPE_INVERSE, l);
+        if (half) rotate8<true>(v, lr);
+        else rotate8<false>(v, lr);
       }
       if (row < nblk) {
         const int s = first + blk0 + row, pi = s / a.P;
         const int hp = min(a.held[b], a.max_pages);
         const int id = pi < hp ? a.table[static_cast<size_t>(b) * a.max_pages + pi] : -1;
         if (id >= 0 && id < a.N)
-          Vec8<T_>::store(static_cast<T_*>(a.pool) + (static_cast<size_t>(id) * a.P + s % a.P) * D + l * 8, v);
+          store8<true>(static_cast<T_*>(a.pool) + (static_cast<size_t>(id) * a.P + s % a.P) * D + own.a, own.b - own.a, v);
         else if (l == 0)
           atomicCAS(a.status, 0, CSA_ERR_NO_SPACE | (1 << 8));
       }
