@@ -9,8 +9,8 @@
 // runs of a block are summed in parallel.
 //
 // Bound by HBM: a and z are read once.  D / 4 lanes hold a row and a thread walks the
-// 16 tokens of one run, four tokens of loads ahead of its arithmetic (2 x 128K tokens
-// of 128 channels: 3.9 TB/s, against 6.6 for a copy; ten instructions a value and
+// 16 tokens of one run, two tokens of loads ahead of its arithmetic (2 x 128K tokens
+// of 128 channels: 4.6 TB/s, against 6.6 for a copy; ten instructions a value and
 // the joins at the end of each block share the SM with the loads).
 #include <cfloat>
 
@@ -20,10 +20,12 @@ namespace csa {
 
 constexpr int kRun = 16;     // tokens per run
 // Runs (of one or more blocks) a CTA sums at once, and threads an SM holds at least: small
-// CTAs, whose sums and joins overlap each other's (for 2 x 128K tokens 35.7 us with
-// 8 runs, 32.6 us with 4; 512 or 1024 threads an SM: 39.9, 37.3 us).
+// CTAs, whose sums and joins overlap each other's (for 2 x 128K tokens 34.1 us with
+// 8 runs, 27.4 us with 4; 640, 768 or 1024 threads an SM: 30.3, 30.6, 31.0 us).  Blocks of
+// one run, of which a CTA takes four (2 x 128K tokens, m = 4: 62.5 us, 65 with 896
+// threads, 78 with 640; 81 with a token's loads at a time and sums through shared memory).
 constexpr int kSlots = 4;
-constexpr int kSmThreads = 768;
+constexpr int kSmThreads = 896, kSmThreadsOne = 768;
 
 struct AppendArgs {
   const void* a;
@@ -128,23 +130,32 @@ __device__ __forceinline__ void join(float& M, float& Z, float& A, float m2, flo
   M = mx;
 }
 
-// One token after the other.
-template <typename T_, int D, bool CAREFUL>
+// Part of a run, kBatch tokens of loads at a time.
+template <typename T_, int D, bool CAREFUL, int kBatch>
 __device__ __forceinline__ void add_tokens(State4& st, const T_* z, const T_* a, int t0, int t1) {
 #pragma unroll 1
-  for (int t = t0; t < t1; ++t) {
-    float z4[4], a4[4];
-    Raw4<T_> zr, ar;
-    zr.load(z + static_cast<size_t>(t) * D);
-    ar.load(a + static_cast<size_t>(t) * D);
-    zr.get(z4);
-    ar.get(a4);
+  for (int t = t0; t < t1; t += kBatch) {
+    Raw4<T_> zr[kBatch], ar[kBatch];
 #pragma unroll
-    for (int c = 0; c < 4; c += 2) add_token2<CAREFUL>(st.M + c, st.Z + c, st.A + c, z4 + c, a4 + c);
+    for (int i = 0; i < kBatch; ++i) {
+      if (t + i < t1) {
+        zr[i].load(z + static_cast<size_t>(t + i) * D);
+        ar[i].load(a + static_cast<size_t>(t + i) * D);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (t + i >= t1) break;
+      float z4[4], a4[4];
+      zr[i].get(z4);
+      ar[i].get(a4);
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) add_token2<CAREFUL>(st.M + c, st.Z + c, st.A + c, z4 + c, a4 + c);
+    }
   }
 }
 // A whole run: the next kAhead tokens are on their way while these are added.
-constexpr int kAhead = 4;
+constexpr int kAhead = 2;
 template <typename T_, int D>
 __device__ __forceinline__ void add_run(State4& st, const T_* z, const T_* a) {
   Raw4<T_> zr[2][kAhead], ar[2][kAhead];
@@ -172,7 +183,7 @@ __device__ __forceinline__ void add_run(State4& st, const T_* z, const T_* a) {
 
 // E blocks a CTA, kSlots / E runs of each at once.
 template <typename T_, int D, int E>
-__global__ void __launch_bounds__(kSlots * D / 4, kSmThreads / (kSlots * D / 4)) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kSlots * D / 4, (E == kSlots ? kSmThreadsOne : kSmThreads) / (kSlots * D / 4)) append_kernel(const AppendArgs a) {
   constexpr int G = D / 8, L = D / 4, SG = kSlots / E;
   __shared__ float part[kSlots][3][D];
   __shared__ float entry[E][D];
@@ -231,14 +242,22 @@ __global__ void __launch_bounds__(kSlots * D / 4, kSmThreads / (kSlots * D / 4))
         };
         start();
         if (t1 - t0 == kRun) add_run<T_, D>(st, za + static_cast<size_t>(t0) * D, aa + static_cast<size_t>(t0) * D);
-        else add_tokens<T_, D, false>(st, za, aa, t0, t1);
+        else add_tokens<T_, D, false, E == kSlots ? 4 : 1>(st, za, aa, t0, t1);
         bool fine = true;
 #pragma unroll
         for (int c = 0; c < 4; ++c) fine = fine && fabsf(st.A[c]) <= FLT_MAX;
         if (!fine) {
           start();
-          add_tokens<T_, D, true>(st, za, aa, t0, t1);
+          add_tokens<T_, D, true, 1>(st, za, aa, t0, t1);
         }
+      }
+      if (E == kSlots && job != 0) {
+        // a block is one run: its sums are the entry's
+        float v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = st.Z[c] == 0.f ? 0.f : __fdiv_rn(st.A[c], st.Z[c]);
+        store4(&entry[slot][q * 4], v);
+        break;
       }
       store4(&part[slot][0][q * 4], st.M);
       store4(&part[slot][1][q * 4], st.Z);
@@ -273,7 +292,7 @@ __global__ void __launch_bounds__(kSlots * D / 4, kSmThreads / (kSlots * D / 4))
     }
 #pragma unroll
     for (int k = 0; k < E; ++k)
-      if (ch < D) entry[k][ch] = Z[k] == 0.f ? 0.f : __fdiv_rn(A[k], Z[k]);
+      if (ch < D && !(E == kSlots && job != 0)) entry[k][ch] = Z[k] == 0.f ? 0.f : __fdiv_rn(A[k], Z[k]);
     __syncthreads();
     // row k of lanes finishes entry k (whole warps take part: rows behind the last are zeros)
     if (threadIdx.x < (E * G + 31) / 32 * 32) {

@@ -144,7 +144,8 @@ __device__ __forceinline__ void lane_rope(LaneRope& lr, long long pos, const dou
     }
   }
 }
-// The same where the warp's rows are at different positions: a lane forms what it meets.
+// The same where the warp's rows are at different positions: a lane forms what it meets
+// (fewer registers than sharing them within a row).
 template <int D>
 __device__ __forceinline__ void lane_rope_alone(LaneRope& lr, long long pos, const double* inv_freq, int R, bool inverse,
                                                 int l) {
