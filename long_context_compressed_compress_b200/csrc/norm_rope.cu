@@ -7,7 +7,7 @@
 // 16-byte (bf16) loads, so a warp moves whole rows; the norm is a shuffle
 // reduction over those lanes.  A warp takes a run of one token's rows: its lanes form
 // the cosines and sines they meet once, keep them in registers, and go through
-// the rows four at a time with all loads under way.  (A CTA-wide table of
+// the rows three or four at a time with all loads under way.  (A CTA-wide table of
 // angles in shared memory cost a barrier and half the occupancy: 355 to 646 us for
 // 32768 tokens of 64 heads.)
 #include <type_traits>
@@ -35,12 +35,15 @@ struct NormRopeArgs {
   uint32_t items;
 };
 
-constexpr int kNrThreads = 256;
-constexpr int kFlight = 4;
+// (32768 tokens of 64 heads: 195 us with 256 threads a CTA.)
+constexpr int kNrThreads = 128;
 
 template <typename T_, int D, bool HALF>
-__global__ void __launch_bounds__(kNrThreads, sizeof(T_) == 2 ? 4 : 3) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrThreads, sizeof(T_) == 2 ? 8 : 6) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int G = D / 8, RW = 32 / G;       // lanes a row, rows a warp
+  // loads under way (64233 tokens of 16 heads, split halves: 123 us with four, 112 with three;
+  // neighbours 109 and 106, but 64 heads 191 and 195)
+  constexpr int kFlight = HALF ? 3 : 4;
   const int lane = threadIdx.x & 31, l = lane % G, sub = lane / G;
   const uint32_t item = blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
   if (item >= a.items) return;
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T_) == 2 ? 4 : 3) norm_rope
 // bound such calls.  (293184 tokens of a head and a key, D = 64, split halves: 58 us, 203
 // with a token a warp.)
 template <typename T_, int D, bool HALF, int TOK>
-__global__ void __launch_bounds__(kNrThreads, 4) norm_rope_few_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrThreads, 8) norm_rope_few_kernel(const NormRopeArgs a) {
   constexpr int G = D / 8, RW = 32 / G, RP = RW / TOK;
   const int lane = threadIdx.x & 31, l = lane % G, r = lane / G % RP;
   const uint32_t item = blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
