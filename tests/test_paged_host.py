@@ -180,3 +180,10 @@ def test_pages_pins():
     assert p.pool[0, 3, 0, 0] == p.pool[0, 1, 0, 0] and p.pool[0, 3, 1, 0] == 7.0
     p.free([0])
     assert p.compact() == 2 and p.rows[1] == [0, 1] and p.ref == [1, 1, 0, 0, 0, 0]
+
+
+def test_groups_say_who_is_attended():
+    from long_context_compressed_compress_b200 import paged
+    assert paged.PrefixGroups([([2, 0], 3), ([1], 0)], 3, device="cpu").attended is None
+    assert paged.PrefixGroups([([3], 0), ([0], 5)], 5, device="cpu").attended.tolist() == [1, 0, 0, 1, 0]
+    assert paged.PrefixGroups([], 2, device="cpu").attended.tolist() == [0, 0]
