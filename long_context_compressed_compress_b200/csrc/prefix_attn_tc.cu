@@ -35,7 +35,7 @@
 // cores with a running maximum; a weight below 2^-126 of the first tile's
 // largest is lost against it anyway.  So once M is there a tile needs no maximum and no
 // word from the tiles before (a running one took a third of a tile's time).
-// P is rounded to bf16 for the MMA (a half step of 2^-9 a weight, of the size
+// P is rounded to bf16 for the MMA (a half step of 2^-8 a weight, of the size
 // of the output's own rounding).  A row has two sums of its weights, by tile parity
 // (i / c) % 2: as rounded, the output's denominator, so that what all of a row's
 // weights have in common cancels; and in fp32 before it, for lse.
