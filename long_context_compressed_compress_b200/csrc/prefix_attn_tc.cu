@@ -45,7 +45,7 @@
 // Roles (12 warps).  Softmax warpgroups 0 and 1 (warps 0 - 3, 4 - 7) take the even
 // and the odd tiles, a thread a row; S and P are double buffered, O is one.  Before
 // that they load Q and the first run tiles, a warp a run, by 16-byte asynchronous
-// copies (one warp took 4700 cycles for a tile); warp 9 loads the further ones.  Warp 8
+// copies (one warp took 4700 cycles for a tile); warps 8 and 9 load the further ones.  Warp 8
 // loads entries: by TMA boxes of a page (or the largest power of two of its rows),
 // row by row where a page is missing.  Warp 10 issues QK (a warpgroup's next as soon
 // as it has read the last S), warp 11 PV.
@@ -338,32 +338,55 @@ __device__ __forceinline__ void push_to_peer(uint32_t dst, const void* src, uint
 // ----------------------------------------------------------------- set-up
 // Where group g's members start (kept within the list).
 __device__ __forceinline__ int group_start(const Args& a, int g) {
-  if (a.G == 1) return g * a.n_seq;
   return min(max(a.group_off[g], 0), a.n_seq);
 }
 
-// Warp 0: the job's group and tile of pairs (jobs are numbered group by group); false
-// when there is no such job.
+// A warp: the job's group and tile of pairs (jobs are numbered group by group); false
+// when there is no such job.  Four groups a lane (1024 groups of a sequence each, 64 heads:
+// 117 us with one, 85).
 __device__ bool find_job(const Args& a, int job, Smem* sm, int* start, int* count) {
   const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int g0 = 0; g0 < a.G; g0 += 32) {
-    const int g = g0 + lane;
-    int jobs = 0, o0 = 0, n = 0;
-    if (g < a.G) {
-      o0 = group_start(a, g);
-      n = max(group_start(a, g + 1) - o0, 0);
-      jobs = static_cast<int>((static_cast<uint32_t>(n) * a.T + a.ppt - 1) / static_cast<uint32_t>(a.ppt));
+  if (a.G == 1) {
+    if (sm != nullptr && lane == 0) {
+      sm->group = 0;
+      sm->tile = job;
     }
-    const int incl = warp_incl_scan(jobs);
+    __syncwarp();
+    *start = 0;
+    *count = a.n_seq;
+    return static_cast<long long>(job) * a.ppt < static_cast<long long>(a.n_seq) * a.T;
+  }
+  int before = 0;
+  for (int g0 = 0; g0 < a.G; g0 += 128) {
+    const int g = g0 + 4 * lane;
+    int o[5], jobs[4], all = 0;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) o[k] = group_start(a, min(g + k, a.G));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      jobs[k] = static_cast<int>((static_cast<uint32_t>(max(o[k + 1] - o[k], 0)) * a.T + a.ppt - 1) /
+                                 static_cast<uint32_t>(a.ppt));
+      all += jobs[k];
+    }
+    const int incl = warp_incl_scan(all);
     const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > job);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      if (sm != nullptr && lane == src) {
-        sm->group = g;
-        sm->tile = job - (before + incl - jobs);
+      int at = before + incl - all, k = 0, first = o[0], n = max(o[1] - o[0], 0);
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        if (k == x && at + jobs[x] <= job) {
+          at += jobs[x];
+          k = x + 1;
+          first = o[x + 1];
+          n = max(o[x + 2] - o[x + 1], 0);
+        }
       }
-      *start = __shfl_sync(0xffffffffu, o0, src);
+      if (sm != nullptr && lane == src) {
+        sm->group = g + k;
+        sm->tile = job - at;
+      }
+      *start = __shfl_sync(0xffffffffu, first, src);
       *count = __shfl_sync(0xffffffffu, n, src);
       __syncwarp();
       return true;
