@@ -68,30 +68,33 @@ class PagedEntries:
         # one list item per row at most does useful work
         self.ws = torch.empty((ops.kv_pages_workspace_size(N, R) // 4,), dtype=torch.int32, device=device)
 
-    def _list(self, v):
+    def _list(self, v, stream=None):
         if torch.is_tensor(v):
             return v
-        return torch.tensor([int(x) for x in v], dtype=torch.int32).to(self.pool.device)
+        # The copy lives until the call returns, its kernels read it later: it is made on
+        # their stream, where its memory comes back into use behind them alone.
+        with torch.cuda.stream(stream):
+            return torch.tensor([int(x) for x in v], dtype=torch.int32).to(self.pool.device)
 
-    def _rows(self, v):
-        v = self._list(v)
+    def _rows(self, v, stream=None):
+        v = self._list(v, stream)
         if v.numel() > self.R:
             raise ValueError(f"a list of {v.numel()} rows for a cache of {self.R}")
         return v
 
     def reserve(self, rows, n_entries, stream=None):
         """Grow rows so that they hold n_entries entries each."""
-        ops.kv_pages_reserve(self._rows(rows), self._list(n_entries), self.P, self.table, self.held, self.refcount,
-                             self.ws, self.status, stream)
+        ops.kv_pages_reserve(self._rows(rows, stream), self._list(n_entries, stream), self.P, self.table, self.held,
+                             self.refcount, self.ws, self.status, stream)
 
     def fork(self, src, dst, n_entries, stream=None):
         """Empty rows dst take the first n_entries entries of rows src."""
-        ops.kv_pages_fork(self._list(src), self._rows(dst), self._list(n_entries), self.pool, self.table, self.held,
-                          self.refcount, self.ws, self.status, stream)
+        ops.kv_pages_fork(self._list(src, stream), self._rows(dst, stream), self._list(n_entries, stream), self.pool,
+                          self.table, self.held, self.refcount, self.ws, self.status, stream)
 
     def free(self, rows, stream=None):
         """Rows give up their pages."""
-        ops.kv_pages_free(self._rows(rows), self.table, self.held, self.refcount, self.status, stream)
+        ops.kv_pages_free(self._rows(rows, stream), self.table, self.held, self.refcount, self.status, stream)
 
     def compact(self, stream=None):
         """Move the pages in use to the lowest ids; n_live receives their number."""
