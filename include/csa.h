@@ -500,8 +500,10 @@ int hca_prefix_attn_fwd(const void* q, const void* pool, int N, int P,
  * kv_pages_fork: the empty row dst[i] becomes a copy of the first n_entries[i]
  * entries of row src[i]: whole pages are shared (refcount + 1), a partial last
  * page is copied, in every layer, to a page of its own.  page_bytes is one
- * layer's page (a multiple of 16 P); layers are N * page_bytes apart.  Site 2: a
- * row out of range, dst not empty or listed twice, or src holding too few pages.
+ * layer's page (a multiple of 16 P); layers are N * page_bytes apart.  The first
+ * int32 of the workspace receives how many forks were made: n, or 0 where the list
+ * was refused (n = 0 leaves it alone).  Site 2: a row out of range, dst not empty
+ * or listed twice, or src holding too few pages.
  *
  * kv_pages_free: every row in the list gives up its pages (refcount - 1) and
  * becomes empty; a row listed twice is freed once.  Site 3: a row out of range.

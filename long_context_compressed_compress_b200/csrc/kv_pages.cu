@@ -67,10 +67,10 @@ struct MetaArgs {
   int32_t* table;
   int32_t* held;
   int32_t* refcount;
+  int32_t* copies;           // workspace [1 + 3 n]: fork's copies: count, then (from, to, rows)
   int32_t* off;              // workspace [n]: first new page of list item i, or -1 while unclaimed
   int32_t* cnt;              // workspace [n]: its number of new pages
   int32_t* list;             // workspace [N]: free pages
-  int32_t* copies;           // workspace [1 + 3 n]: fork's copies: count, then (from, to, rows)
   int* status;
 };
 
@@ -297,7 +297,7 @@ using namespace csa;
 
 extern "C" size_t kv_pages_workspace_size(int N, int n) {
   if (N < 0 || n < 0) return 0;
-  // grow: off, cnt [n], list [N], copies [1 + 3 n]; compact: count, moves [2 N], map [N]
+  // grow: copies [1 + 3 n], off, cnt [n], list [N]; compact: count, moves [2 N], map [N]
   return 4 * (3 * static_cast<size_t>(N) + 5 * static_cast<size_t>(n) + 4);
 }
 
@@ -313,10 +313,10 @@ static int grow(bool fork, const int32_t* src, const int32_t* dst, const int32_t
   MetaArgs a;
   a.src = src; a.dst = dst; a.n_entries = n_entries; a.n = n; a.P = P; a.R = R; a.max_pages = max_pages; a.N = N;
   a.table = table; a.held = held; a.refcount = refcount;
-  a.off = static_cast<int32_t*>(workspace);
+  a.copies = static_cast<int32_t*>(workspace);      // (first: callers may read the count)
+  a.off = a.copies + 1 + 3 * static_cast<size_t>(n);
   a.cnt = a.off + n;
-  a.copies = a.cnt + n;
-  a.list = a.copies + 1 + 3 * static_cast<size_t>(n);
+  a.list = a.cnt + n;
   a.status = status_word(status);
   CSA_REQUIRE(a.status != nullptr, CSA_ERR_CUDA);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -452,20 +452,27 @@ class HcaDecode:
         """Complete entries of every row, int32 [R] (what a fork shares)."""
         return torch.div(self.pos, self.cfg.m, rounding_mode="floor").to(torch.int32)
 
-    def copy_state(self, src, dst):
+    def copy_state(self, src, dst, done=None):
         """Rows dst take the window, carry and position of rows src (int64 index
-        tensors); the entries are the cache's to fork."""
+        tensors), unless ``done`` (bool [1] on the device) says otherwise; the entries
+        are the cache's to fork."""
         for t in (self.pos, self.ring, self.carry):
-            t[dst] = t[src]
+            new = t[src]
+            if done is not None:
+                new = torch.where(done.view([1] * new.dim()), new, t[dst])
+            t[dst] = new
 
     def fork(self, src, dst):
         """Empty rows dst (lists or int32 tensors) become copies of rows src: whole
         pages shared, the last partial page and the rest of the state copied.  A
+        list that the cache refuses (its status word says why) changes nothing.  A
         cache of several layers is forked once, the other layers' states copied by
-        their own ``copy_state``."""
+        their own ``copy_state(src, dst, cache.forked())``."""
         src, dst = self.cache._list(src), self.cache._list(dst)
+        if not dst.numel():
+            return
         self.cache.fork(src, dst, self.entries()[src.long()])
-        self.copy_state(src.long(), dst.long())
+        self.copy_state(src.long(), dst.long(), self.cache.forked())
 
     def capture(self, x):
         """Record one step on static input buffers ``x`` into a CUDA graph (run

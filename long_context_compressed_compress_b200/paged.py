@@ -92,6 +92,11 @@ class PagedEntries:
         ops.kv_pages_fork(self._list(src, stream), self._rows(dst, stream), self._list(n_entries, stream), self.pool,
                           self.table, self.held, self.refcount, self.ws, self.status, stream)
 
+    def forked(self):
+        """Whether the cache's last call, a fork, was made (a refused one changes
+        nothing): bool [1] on the device."""
+        return self.ws[:1] > 0
+
     def free(self, rows, stream=None):
         """Rows give up their pages."""
         ops.kv_pages_free(self._rows(rows, stream), self.table, self.held, self.refcount, self.status, stream)

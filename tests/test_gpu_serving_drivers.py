@@ -44,3 +44,91 @@ def test_host_lists_on_a_busy_side_stream(mods):
         np.testing.assert_array_equal(c.held.cpu().numpy(), [len(r) for r in m.rows])
         np.testing.assert_array_equal(c.table.cpu().numpy(), m.table())
         np.testing.assert_array_equal(c.refcount.cpu().numpy(), m.ref)
+
+
+def decode(mods, R=6, N=200, P=4, m=8, W=20, H=8, D=128, dt=torch.bfloat16, L=1, layer_at=0, cache=None, **kw):
+    layer, _, paged = mods
+    from long_context_compressed_compress_b200 import configs
+    cfg = configs._hca(B=R, T=1024, H=H, D=D, m=m, W=W, dtype="bf16" if dt is torch.bfloat16 else "f32", tau=0.1)
+    cache = cache or paged.PagedEntries(L, N, P, D, R, cfg.S, dtype=dt)
+    return cache, layer.HcaDecode(cfg, cache, layer=layer_at, **kw)
+
+
+def tokens(R, T, D=128, dt=torch.bfloat16, seed=0, H=8):
+    g = torch.Generator().manual_seed(seed)
+    x = {k: torch.randn(R, T, D, generator=g).to(dt).cuda() for k in ("a", "z", "kv_raw")}
+    x["q"] = torch.randn(R, T, H, D, generator=g).to(dt).cuda()
+    return x
+
+
+def one(x, t=0):
+    return {k: v[:, t].contiguous() for k, v in x.items()}
+
+
+def state(d):
+    c = d.cache
+    return [t.clone() for t in (d.pos, d.ring, d.carry, c.held, c.table, c.refcount, c.pool)]
+
+
+def same_state(d, want):
+    assert all(torch.equal(a, b) for a, b in zip(state(d), want))
+
+
+@pytest.mark.parametrize("why", ["dst is live", "no tail page", "src holds too few"])
+def test_a_refused_fork_leaves_both_rows_alone(mods, why):
+    c, d = decode(mods, N=20)
+    c.reserve([0, 3], [60, 17] if why == "no tail page" else [32, 17])    # 15 + 5 or 8 + 5 of 20 pages
+    d.load({k: v for k, v in tokens(6, 45).items() if k != "q"}, torch.tensor([45, 0, 0, 30, 0, 0], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert c.status.item() == 0
+    if why == "src holds too few":
+        c.free([3])
+    before = state(d)
+    src, dst = {"dst is live": ([0, 0], [1, 3]), "no tail page": ([0], [1]), "src holds too few": ([0, 3], [1, 2])}[why]
+    d.fork(src, dst)
+    torch.cuda.synchronize()
+    assert c.status.item() == (6 if why == "no tail page" else 1) | 2 << 8
+    same_state(d, before)
+    # and the rows go on: a fork that can be made
+    c.status.zero_()
+    c.free([3])
+    d.fork([0], [1])
+    torch.cuda.synchronize()
+    assert c.status.item() == 0 and d.pos[1].item() == 45 and c.held[1].item() == 2
+    assert torch.equal(d.ring[1], before[1][0]) and torch.equal(d.carry[1], before[2][0])
+
+
+def test_a_fork_for_two_layers_captured(mods):
+    """The second layer's state goes by the same fork; in a graph, a replay that is
+    refused changes neither."""
+    c, d = decode(mods, L=2)
+    _, e = decode(mods, cache=c, layer_at=1)
+    c.reserve([0], [32])
+    n = torch.tensor([45, 0, 0, 0, 0, 0], dtype=torch.int32).cuda()
+    for k, lay in enumerate((d, e)):
+        lay.load({k_: v for k_, v in tokens(6, 45, seed=k).items() if k_ != "q"}, n)
+    src, dst = (torch.tensor(v, dtype=torch.int32).cuda() for v in ([0, 0], [1, 4]))
+
+    def fork():
+        d.fork(src, dst)
+        e.copy_state(src.long(), dst.long(), c.forked())
+    fork()
+    torch.cuda.synchronize()
+    assert c.status.item() == 0 and d.pos.tolist() == e.pos.tolist() == [45, 45, 0, 0, 45, 0]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        fork()
+    torch.cuda.current_stream().wait_stream(s)
+    before = state(d), state(e)
+    g.replay()                                         # rows 1 and 4 are live
+    torch.cuda.synchronize()
+    assert c.status.item() == 1 | 2 << 8
+    same_state(d, before[0]), same_state(e, before[1])
+    c.status.zero_()
+    dst.copy_(torch.tensor([2, 5], dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    assert c.status.item() == 0 and d.pos.tolist() == e.pos.tolist() == [45, 45, 45, 0, 45, 45]
+    assert torch.equal(e.ring[5], e.ring[0]) and torch.equal(e.carry[2], e.carry[0])

@@ -40,3 +40,38 @@ def test_host_lists_are_made_on_the_stream_of_their_call(mods, monkeypatch, stre
     c.fork([0], [2], [3], stream=stream)
     c.free([0, 1], stream=stream)
     assert seen == [stream] * 6
+
+
+def decode(mods, R=4, **kw):
+    layer, _, paged = mods
+    from long_context_compressed_compress_b200 import configs
+    cfg = configs._hca(B=R, T=64, H=2, D=64, m=4, W=kw.pop("W", 6), dtype="f32", tau=0.1)
+    d = layer.HcaDecode(cfg, cache(paged, R), device="cpu", groups=kw.pop("groups", None) or
+                        paged.PrefixGroups.singles(R, device="cpu"), **kw)
+    g = torch.Generator().manual_seed(3)
+    d.pos.copy_(torch.randint(1, 60, d.pos.shape, generator=g))
+    for t in (d.ring, d.carry):
+        t.copy_(torch.randn(t.shape, generator=g))
+    return d
+
+
+@pytest.mark.parametrize("src,dst", [([0, 0], [1, 3]), ([2], [0]), ([], [])])
+@pytest.mark.parametrize("made", [True, False])
+def test_fork_copies_the_state_only_where_the_pages_were_forked(mods, monkeypatch, src, dst, made):
+    _, ops, _ = mods
+    d = decode(mods)
+    calls = []
+
+    def fork(s, t, n, *a):
+        calls.append((s.tolist(), t.tolist(), n.tolist()))
+        d.cache.ws[0] = len(t) if made else 0
+    monkeypatch.setattr(ops, "kv_pages_fork", fork)
+    before = [t.clone() for t in (d.pos, d.ring, d.carry)]
+    d.cache.ws.fill_(0 if made else 7)
+    d.fork(src, dst)
+    assert calls == ([(src, dst, [int(before[0][i]) // 4 for i in src])] if dst else [])
+    for t, b in zip((d.pos, d.ring, d.carry), before):
+        want = b.clone()
+        if made:
+            want[dst] = b[src]
+        assert torch.equal(t, want)
