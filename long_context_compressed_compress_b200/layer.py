@@ -455,12 +455,18 @@ class HcaDecode:
     def copy_state(self, src, dst, done=None):
         """Rows dst take the window, carry and position of rows src (int64 index
         tensors), unless ``done`` (bool [1] on the device) says otherwise; the entries
-        are the cache's to fork."""
+        are the cache's to fork.  With ``done`` the rows may be out of range where it
+        is false, as those of a refused list."""
+        if done is not None:      # (indexing itself would stop the device)
+            src, dst = (self._in_range(i) for i in (src, dst))
         for t in (self.pos, self.ring, self.carry):
             new = t[src]
             if done is not None:
                 new = torch.where(done.view([1] * new.dim()), new, t[dst])
             t[dst] = new
+
+    def _in_range(self, rows):
+        return rows.long().clamp(0, self.cache.R - 1)
 
     def fork(self, src, dst):
         """Empty rows dst (lists or int32 tensors) become copies of rows src: whole
@@ -471,8 +477,8 @@ class HcaDecode:
         src, dst = self.cache._list(src), self.cache._list(dst)
         if not dst.numel():
             return
-        self.cache.fork(src, dst, self.entries()[src.long()])
-        self.copy_state(src.long(), dst.long(), self.cache.forked())
+        self.cache.fork(src, dst, self.entries()[self._in_range(src)])
+        self.copy_state(src, dst, self.cache.forked())
 
     def capture(self, x):
         """Record one step on static input buffers ``x`` into a CUDA graph (run

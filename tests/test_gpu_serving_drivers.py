@@ -132,3 +132,16 @@ def test_a_fork_for_two_layers_captured(mods):
     torch.cuda.synchronize()
     assert c.status.item() == 0 and d.pos.tolist() == e.pos.tolist() == [45, 45, 45, 0, 45, 45]
     assert torch.equal(e.ring[5], e.ring[0]) and torch.equal(e.carry[2], e.carry[0])
+
+
+@pytest.mark.parametrize("src,dst", [([9], [1]), ([-1], [1]), ([0, 1], [2, 6]), ([0], [-3]), ([2 ** 31 - 1], [-2 ** 31])])
+def test_a_fork_of_rows_out_of_range_is_refused(mods, src, dst):
+    c, d = decode(mods)
+    c.reserve([0], [32])
+    d.load({k: v for k, v in tokens(6, 20).items() if k != "q"}, torch.tensor([20, 0, 0, 0, 0, 0], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    before = state(d)
+    d.fork(src, dst)
+    torch.cuda.synchronize()
+    assert c.status.item() == 1 | 2 << 8
+    same_state(d, before)

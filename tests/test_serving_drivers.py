@@ -75,3 +75,17 @@ def test_fork_copies_the_state_only_where_the_pages_were_forked(mods, monkeypatc
         if made:
             want[dst] = b[src]
         assert torch.equal(t, want)
+
+
+@pytest.mark.parametrize("src,dst", [([9], [1]), ([-1], [1]), ([0, 1], [2, 4]), ([0], [-3]), ([2 ** 31 - 1], [-2 ** 31])])
+def test_fork_of_rows_out_of_range_reaches_the_cache(mods, monkeypatch, src, dst):
+    """The cache refuses them (and records why); no indexing by them, which on a GPU
+    would end the process."""
+    _, ops, _ = mods
+    d = decode(mods)
+    calls = []
+    monkeypatch.setattr(ops, "kv_pages_fork", lambda s, t, *a: (calls.append((s.tolist(), t.tolist())), d.cache.ws[:1].zero_()))
+    before = [t.clone() for t in (d.pos, d.ring, d.carry)]
+    d.fork(src, dst)
+    assert calls == [(src, dst)]
+    assert all(torch.equal(a, b) for a, b in zip((d.pos, d.ring, d.carry), before))
