@@ -360,12 +360,15 @@ int grouped_out_proj(const void* o, int M, int H, int D, int groups, int d_g,
 /*
  * Decode-step helpers (state update of the KV cache tiers, [cf-1] §4.4):
  * csa_ring_append writes rows[b, :] (dtype, [B, D]) into ring[b, pos[b] % cap, :];
- * csa_pos_advance adds delta to each pos[b].  Both read positions on the device,
- * so a captured CUDA graph of a decode step stays valid from step to step.
+ * csa_pos_advance adds delta to each pos[b], csa_pos_advance_rows delta[b] (int32
+ * [B] on the device; 0 for an idle row).  All read positions on the device, so a
+ * captured CUDA graph of a decode step stays valid from step to step.
  */
 int csa_ring_append(const void* rows, int dtype, int B, int D, void* ring,
                     int cap, const int32_t* pos, csa_stream_t stream);
 int csa_pos_advance(int32_t* pos, int B, int delta, csa_stream_t stream);
+int csa_pos_advance_rows(int32_t* pos, int B, const int32_t* delta,
+                         csa_stream_t stream);
 
 /*
  * csa_state_gather -- snapshots of a layer's decode-time state, the tier of

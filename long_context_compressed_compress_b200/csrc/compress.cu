@@ -294,6 +294,10 @@ __global__ void pos_advance_kernel(int32_t* pos, int B, int delta) {
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i < B) pos[i] += delta;
 }
+__global__ void pos_advance_rows_kernel(int32_t* pos, int B, const int32_t* delta) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < B) pos[i] += delta[i];
+}
 
 
 // ---------------------------------------------------------------------------
@@ -632,6 +636,13 @@ int csa_pos_advance(int32_t* pos, int B, int delta, csa_stream_t stream) {
   CSA_REQUIRE(pos != nullptr && B >= 0, CSA_ERR_INVALID_ARG);
   if (B == 0) return CSA_OK;
   pos_advance_kernel<<<(B + 255) / 256, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(pos, B, delta);
+  return check_launch();
+}
+
+int csa_pos_advance_rows(int32_t* pos, int B, const int32_t* delta, csa_stream_t stream) {
+  CSA_REQUIRE(pos != nullptr && delta != nullptr && B >= 0, CSA_ERR_INVALID_ARG);
+  if (B == 0) return CSA_OK;
+  pos_advance_rows_kernel<<<(B + 255) / 256, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(pos, B, delta);
   return check_launch();
 }
 

@@ -380,13 +380,13 @@ class HcaDecode:
     of a row's state is here: pos int32 [R] (tokens seen), the raw window ring
     [R, W, D] and the compressor's carry [R, 2, 3, D].  ``groups``
     (paged.PrefixGroups, default: every row by itself) names the rows that share
-    their first pages and, by leaving rows out, those that are idle: their
-    outputs are left as they were (their state advances all the same).
+    their first pages and, by leaving rows out, those that are idle: a step leaves
+    their outputs, state and pages as they were and does not look at their input.
 
         qk_norm_rope or csa_ring_append   token's raw KV -> ring slot pos % W
         hca_paged_append                  block pooling; a completed entry -> its page
         hca_prefix_attn_fwd               out [R, 1, H, D] (window + sink fused)
-        csa_pos_advance                   pos += 1 on the device
+        csa_pos_advance                   pos += 1 on the device, but for idle rows
 
     Every launch reads positions and pages on the device, so the step can be captured
     in a CUDA graph (``capture``) and replayed; a capture holds its ``groups``."""
@@ -428,24 +428,28 @@ class HcaDecode:
         c = self.cfg
         t = timer or _no_timer
         R = self.cache.R
+        live = self.groups.attended           # (as lengths: one token, or none; None: all rows)
         q, raw = x["q"].view(R, 1, c.H, c.D), x["kv_raw"].view(R, 1, c.D)
         if self.norm_rope is not None:
             with t("qk_norm_rope"):
-                self.norm_rope.queries(q, raw, self.q_n, self.ring, self.pos)
+                self.norm_rope.queries(q, raw, self.q_n, self.ring, self.pos, live)
             q = self.q_n
+        elif live is not None:
+            with t("qk_norm_rope"):           # (a plain copy)
+                NormRope(norm=False).queries(None, raw, None, self.ring, self.pos, live)
         else:
             with t("csa_ring_append"):
                 ops.csa_ring_append(x["kv_raw"], self.ring, self.pos)
         with t("hca_paged_append"):
-            self._append(x["a"].view(R, 1, c.D), x["z"].view(R, 1, c.D))
+            self._append(x["a"].view(R, 1, c.D), x["z"].view(R, 1, c.D), live)
         with t("hca_prefix_attn_fwd"):
             ops.hca_prefix_attn_fwd(q, self.cache.pool[self.layer], self.cache.table, self.cache.held, self.groups,
                                     self.ring, self.sink, c.tau, c.W, self.pos, self.out, c.m, lse=self.lse,
                                     status=self.cache.status)
         if self.norm_rope is not None:
-            self.norm_rope.back(self.out, self.pos, self.groups.attended)
+            self.norm_rope.back(self.out, self.pos, live)
         with t("csa_pos_advance"):
-            ops.csa_pos_advance(self.pos, 1)
+            ops.csa_pos_advance(self.pos, 1 if live is None else live)
         return self.out
 
     def entries(self):

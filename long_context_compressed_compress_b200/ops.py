@@ -59,6 +59,7 @@ _SIGS = {
     "swa_sink_merge": ([P, P, P, P, P, F, I, I, I, I, I, I, I, I, P, P, I, P], I),
     "csa_ring_append": ([P, I, I, I, P, I, P, P], I),
     "csa_pos_advance": ([P, I, I, P], I),
+    "csa_pos_advance_rows": ([P, I, P, P], I),
     "csa_decode_update": ([P] * 8 + [I] * 8 + [P] * 12 + [F, P, P], I),
     "csa_state_gather": ([P, I, I, I, I, P, I, I, I, P, I, P], I),
     "qk_norm_rope": ([P, I64, I64, P, I64, I64, I, I, I, I, I, P, P, I, P, I, P, P, F, I, P, P, I, P], I),
@@ -253,6 +254,12 @@ def csa_decode_update(x, carry, ring, kv_c, k_fp4, k_sf, q_fp4, q_sf, pos, m, gs
 
 
 def csa_pos_advance(pos, delta=1, stream=None):
+    """pos [B] += delta, a number or an int32 [B] tensor."""
+    if torch.is_tensor(delta):
+        dev, n = _home(pos), pos.numel()
+        _check("csa_pos_advance_rows", lib.csa_pos_advance_rows(
+            _arg(pos, "pos", torch.int32, (n,), dev), n, _arg(delta, "delta", torch.int32, (n,), dev), _on(stream, dev)))
+        return
     _check("csa_pos_advance", lib.csa_pos_advance(_ptr(pos), pos.numel(), delta, _stream(stream)))
 
 

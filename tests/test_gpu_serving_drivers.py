@@ -145,3 +145,67 @@ def test_a_fork_of_rows_out_of_range_is_refused(mods, src, dst):
     torch.cuda.synchronize()
     assert c.status.item() == 1 | 2 << 8
     same_state(d, before)
+
+
+def rope(layer, D=128, R=32):
+    f = torch.tensor([10000.0 ** (-2.0 * i / R) for i in range(R // 2)], dtype=torch.float64)
+    return layer.NormRope(inv_freq=f.cuda(), kv_weight=torch.linspace(0.5, 1.5, D).cuda())
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("nr", [False, True])
+def test_idle_rows_stay_as_they_are(mods, nr, dt):
+    """A freed row and an idle one that holds pages, over more steps than a block has
+    tokens, some of them replayed: nothing is reported, their state, pages and outputs
+    stay, and NaN in their input reaches nobody; the others go on as in a batch of
+    their own."""
+    layer, ops, paged = mods
+    kw = dict(R=4, dt=dt, norm_rope=rope(layer) if nr else None)
+    c, d = decode(mods, **kw)
+    c2, e = decode(mods, **kw)
+    x = {k: v for k, v in tokens(4, 37, dt=dt).items() if k != "q"}
+    for cc, dd in ((c, d), (c2, e)):
+        cc.reserve([0, 1, 2, 3], [40] * 4)
+        dd.load(x)
+    c.free([1])
+    d.groups = paged.PrefixGroups([([3], 0), ([0], 0)], 4)           # 1 is freed, 2 idle
+    idle = [1, 2]
+    pages = c.table[2, :10].long()
+
+    def kept():
+        return [t[idle].clone() for t in (d.pos, d.ring, d.carry, d.out, c.table, c.held)] + [c.pool[:, pages].clone()]
+    before = kept()
+    static = {k: torch.zeros_like(v) for k, v in one(tokens(4, 1, dt=dt)).items()}
+    y = tokens(4, 20, dt=dt, seed=5)
+    for t in range(20):
+        for k in static:
+            static[k].copy_(y[k][:, t])
+        want = e.step(static).clone()
+        for k in static:
+            static[k][idle] = float("nan")
+        if t == 10:
+            d.capture(static)
+        got = d.step(static) if t < 10 else d.replay()
+        assert torch.equal(got[[0, 3]], want[[0, 3]])
+    torch.cuda.synchronize()
+    assert c.status.item() == 0 and d.pos.tolist() == [57, 37, 37, 57]
+    assert all(torch.equal(a, b) for a, b in zip(kept(), before))
+    assert torch.equal(d.ring[[0, 3]], e.ring[[0, 3]]) and torch.equal(d.carry[[0, 3]], e.carry[[0, 3]])
+    # and the idle one is taken up again where it was left
+    d.groups = paged.PrefixGroups([([2], 0)], 4)
+    c2, f = decode(mods, **kw)
+    c2.reserve([0, 1, 2, 3], [40] * 4)
+    f.load(x)
+    for k in static:
+        static[k].copy_(y[k][:, 0])
+    assert torch.equal(d.step(static)[2], f.step(static)[2])
+
+
+def test_positions_advance_by_rows(mods):
+    _, ops, _ = mods
+    p, n = torch.arange(700, dtype=torch.int32).cuda(), (torch.arange(700, dtype=torch.int32) % 3).cuda()
+    want = p + n
+    ops.csa_pos_advance(p, n)
+    assert torch.equal(p, want)
+    ops.csa_pos_advance(p, 2)
+    assert torch.equal(p, want + 2)

@@ -89,3 +89,36 @@ def test_fork_of_rows_out_of_range_reaches_the_cache(mods, monkeypatch, src, dst
     d.fork(src, dst)
     assert calls == [(src, dst)]
     assert all(torch.equal(a, b) for a, b in zip((d.pos, d.ring, d.carry), before))
+
+
+@pytest.mark.parametrize("nr", [False, True])
+def test_a_step_tells_every_call_which_rows_are_idle(mods, monkeypatch, nr):
+    layer, ops, paged = mods
+    seen = {}
+
+    def record(name):
+        return lambda *a, **k: seen.update({name: (a, k)})
+    for name in ("qk_norm_rope", "hca_paged_append", "hca_prefix_attn_fwd", "csa_ring_append", "csa_pos_advance"):
+        monkeypatch.setattr(ops, name, record(name))
+    groups = paged.PrefixGroups([([2, 0], 0)], 4, device="cpu")
+    d = decode(mods, groups=groups, norm_rope=layer.NormRope() if nr else None)
+    d.step({k: torch.zeros(4, 64) for k in ("a", "z", "kv_raw")} | {"q": torch.zeros(4, 2, 64)})
+    live = groups.attended
+    assert live.tolist() == [1, 0, 1, 0]
+    assert seen["qk_norm_rope"][1]["lens"] is live and seen["hca_paged_append"][1]["lens"] is live
+    assert seen["csa_pos_advance"][0][1] is live and "csa_ring_append" not in seen
+    # every row attended: as before
+    seen.clear()
+    d.groups = paged.PrefixGroups.singles(4, device="cpu")
+    d.step({k: torch.zeros(4, 64) for k in ("a", "z", "kv_raw")} | {"q": torch.zeros(4, 2, 64)})
+    assert seen["hca_paged_append"][1]["lens"] is None and seen["csa_pos_advance"][0][1] == 1
+    assert ("qk_norm_rope" if nr else "csa_ring_append") in seen
+
+
+def test_advancing_by_rows_refusals(mods):
+    _, ops, _ = mods
+    f = 1 << 20
+    assert ops.lib.csa_pos_advance_rows(None, 2, f, None) == 1 and ops.lib.csa_pos_advance_rows(f, 2, None, None) == 1
+    assert ops.lib.csa_pos_advance_rows(f, -1, f, None) == 1 and ops.lib.csa_pos_advance_rows(f, 0, f, None) == 0
+    with pytest.raises(ValueError):
+        ops.csa_pos_advance(torch.zeros(2, dtype=torch.int32), torch.ones(2, dtype=torch.int32))
