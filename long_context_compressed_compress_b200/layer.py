@@ -383,7 +383,7 @@ class HcaDecode:
     their first pages and, by leaving rows out, those that are idle: a step leaves
     their outputs, state and pages as they were and does not look at their input.
 
-        qk_norm_rope or csa_ring_append   token's raw KV -> ring slot pos % W
+        qk_norm_rope or csa_ring_append   token's raw KV -> ring slot pos % W (none for W = 0)
         hca_paged_append                  block pooling; a completed entry -> its page
         hca_prefix_attn_fwd               out [R, 1, H, D] (window + sink fused)
         csa_pos_advance                   pos += 1 on the device, but for idle rows
@@ -402,7 +402,8 @@ class HcaDecode:
         self.lse = torch.zeros((R, 1, cfg.H), dtype=torch.float32, device=device) if with_lse else None
         self.q_n = torch.empty_like(self.out) if norm_rope is not None else None
         self.groups = groups or paged.PrefixGroups.singles(R, device=device)
-        self.launches = 4 + (norm_rope.launches - 2 if norm_rope is not None else 0)
+        # the window's, append, attention, positions (with a norm_rope the first is the queries' too)
+        self.launches = 4 + norm_rope.launches - 2 if norm_rope is not None else 4 if cfg.W else 3
         self.graph = self.captured = None
 
     def _append(self, a, z, lens=None):
@@ -418,7 +419,8 @@ class HcaDecode:
         int32 [R] on the device, T for all by default) behind what the rows hold."""
         R, T, _ = x["a"].shape
         nr = self.norm_rope or NormRope(norm=False)
-        nr.queries(None, x["kv_raw"], None, self.ring, self.pos, lens)
+        if self.cfg.W:
+            nr.queries(None, x["kv_raw"], None, self.ring, self.pos, lens)
         self._append(x["a"], x["z"], lens)
         self.pos += T if lens is None else lens.clamp(0, T)
 
@@ -432,8 +434,10 @@ class HcaDecode:
         q, raw = x["q"].view(R, 1, c.H, c.D), x["kv_raw"].view(R, 1, c.D)
         if self.norm_rope is not None:
             with t("qk_norm_rope"):
-                self.norm_rope.queries(q, raw, self.q_n, self.ring, self.pos, live)
+                self.norm_rope.queries(q, raw if c.W else None, self.q_n, self.ring if c.W else None, self.pos, live)
             q = self.q_n
+        elif not c.W:
+            pass                              # no window to keep
         elif live is not None:
             with t("qk_norm_rope"):           # (a plain copy)
                 NormRope(norm=False).queries(None, raw, None, self.ring, self.pos, live)

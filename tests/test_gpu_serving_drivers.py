@@ -209,3 +209,45 @@ def test_positions_advance_by_rows(mods):
     assert torch.equal(p, want)
     ops.csa_pos_advance(p, 2)
     assert torch.equal(p, want + 2)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("nr", [False, True])
+def test_decode_without_a_window(mods, nr, dt):
+    """W = 0: a query sees its complete entries alone (none before the first, which gives
+    0).  Tolerances are the decode driver's: 2e-2 absolute in bf16, 1e-5 in fp32; the
+    logits of rounded entries are off by |q| |k| tau 2^-8 in bf16."""
+    layer, _, paged = mods
+    m, D, H = 8, 128, 8
+    ropes = rope(layer) if nr else None
+    c, d = decode(mods, R=3, m=m, W=0, dt=dt, norm_rope=ropes, with_lse=True)
+    c.reserve([0, 1, 2], [8] * 3)
+    x = tokens(3, 33, dt=dt, seed=2)
+    lens = [25, 0, 7]
+    d.load({k: v[:, :25].contiguous() for k, v in x.items() if k != "q"}, torch.tensor(lens, dtype=torch.int32).cuda())
+    for step in range(4):
+        out = d.step(one(x, 25 + step))
+        torch.cuda.synchronize()
+        for r in range(3):
+            at = list(range(lens[r])) + list(range(25, 26 + step))
+            n, q = len(at), np64(x["q"][r, 25 + step])
+            ent, _ = serving.append(np64(x["z"][r, at]), np64(x["a"][r, at]), n, m)
+            if nr:
+                f = np64(ropes.inv_freq)
+                q = serving.norm_rope(q, np.full(H, n - 1), f)
+                ent = serving.norm_rope(ent, m * np.arange(len(ent)), f)
+                q, ent = (np64(torch.tensor(v).to(dt)) for v in (q, ent))
+            else:
+                ent = np64(torch.tensor(ent).to(dt))
+            ref, lse, _ = serving.attend(q, ent.reshape(-1, D), None, 0.1)
+            if nr:
+                ref = serving.norm_rope(ref, np.full(H, n - 1), f, norm=False, inverse=True)
+            tol = 2e-2 if dt is torch.bfloat16 else 1e-5 * np.maximum(1, np.abs(ref))
+            assert (np.abs(np64(out[r, 0]) - ref) <= tol).all()
+            if n < m:
+                assert (out[r] == 0).all() and (d.lse[r] == -float("inf")).all()
+            else:
+                assert np.abs(np64(d.lse[r, 0]) - lse).max() <= (0.05 if dt is torch.bfloat16 else 1e-4)
+    assert c.status.item() == 0
+    d.fork([0], [1])                                   # (row 1 holds pages: refused)
+    assert c.status.item() == 1 | 2 << 8 and d.pos.tolist() == [29, 4, 11]

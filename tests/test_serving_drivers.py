@@ -122,3 +122,20 @@ def test_advancing_by_rows_refusals(mods):
     assert ops.lib.csa_pos_advance_rows(f, -1, f, None) == 1 and ops.lib.csa_pos_advance_rows(f, 0, f, None) == 0
     with pytest.raises(ValueError):
         ops.csa_pos_advance(torch.zeros(2, dtype=torch.int32), torch.ones(2, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("nr", [False, True])
+def test_without_a_window_there_is_no_ring_to_write(mods, monkeypatch, nr):
+    layer, ops, _ = mods
+    calls = []
+    for name in ("qk_norm_rope", "hca_paged_append", "hca_prefix_attn_fwd", "csa_ring_append", "csa_pos_advance"):
+        monkeypatch.setattr(ops, name, lambda *a, _n=name, **k: calls.append((_n, a)))
+    d = decode(mods, W=0, norm_rope=layer.NormRope() if nr else None)
+    d.load({k: torch.zeros(4, 5, 64) for k in ("a", "z", "kv_raw")})
+    assert [c[0] for c in calls] == ["hca_paged_append"]
+    calls.clear()
+    d.step({k: torch.zeros(4, 64) for k in ("a", "z", "kv_raw")} | {"q": torch.zeros(4, 2, 64)})
+    assert [c[0] for c in calls] == ["qk_norm_rope"] * nr + ["hca_paged_append", "hca_prefix_attn_fwd", "csa_pos_advance"]
+    assert len(calls) == d.launches
+    if nr:
+        assert calls[0][1][1] is None and calls[0][1][3] is None
