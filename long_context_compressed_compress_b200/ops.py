@@ -354,9 +354,13 @@ def qk_norm_rope(q, kv, q_out, kv_out, q_pos0, inv_freq=None, q_weight=None, kv_
         raise ValueError("q with q_out, kv with kv_out, at least one pair")
     x = q if q is not None else kv
     dev, dt = _home(x), x.dtype
-    if not x.numel():
-        return
     B, T, D = x.shape[0], x.shape[1], x.shape[-1]
+    if q is not None and not q.numel():
+        if kv is None:
+            return
+        q = None                     # no heads: the key alone
+    if not B or not T:
+        return
     H = cap = qb = qt = kb = kt = 0
     qp = qop = kp = kop = None
     if q is not None:

@@ -251,3 +251,19 @@ def test_decode_without_a_window(mods, nr, dt):
     assert c.status.item() == 0
     d.fork([0], [1])                                   # (row 1 holds pages: refused)
     assert c.status.item() == 1 | 2 << 8 and d.pos.tolist() == [29, 4, 11]
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_a_key_beside_queries_of_no_heads(mods, dt):
+    """q [B, T, 0, D] beside a key gives what the key alone gives."""
+    layer, ops, _ = mods
+    B, T, D = 2, 9, 64
+    k = torch.randn(B, T, D, generator=torch.Generator().manual_seed(1)).to(dt).cuda()
+    q = torch.empty(B, T, 0, D, dtype=dt, device="cuda")
+    p = torch.tensor([5, 1000], dtype=torch.int32).cuda()
+    f = rope(layer).inv_freq
+    rings = [torch.full((B, 6, D), 7.0, dtype=dt, device="cuda") for _ in range(2)]
+    ops.qk_norm_rope(q, k, torch.empty_like(q), rings[0], p, inv_freq=f)
+    ops.qk_norm_rope(None, k, None, rings[1], p, inv_freq=f)
+    assert torch.equal(*rings) and not (rings[0] == 7.0).any()
+    ops.qk_norm_rope(q, None, torch.empty_like(q), None, p, inv_freq=f)

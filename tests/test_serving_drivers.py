@@ -139,3 +139,26 @@ def test_without_a_window_there_is_no_ring_to_write(mods, monkeypatch, nr):
     assert len(calls) == d.launches
     if nr:
         assert calls[0][1][1] is None and calls[0][1][3] is None
+
+
+class _Lib:
+    """Records calls of one entry point; nothing runs."""
+
+    def __init__(self, monkeypatch, ops, name):
+        self.calls = []
+        monkeypatch.setattr(ops, "_home", lambda t: -1)
+        monkeypatch.setattr(ops, "lib", type("L", (), {name: staticmethod(lambda *a: (self.calls.append(a), 0)[1])}))
+        self.stream = type("S", (), {"cuda_stream": 0})
+
+
+@pytest.mark.parametrize("H,kv,T,calls", [(0, 1, 3, 1), (2, 1, 3, 1), (0, 0, 3, 0), (0, 1, 0, 0), (2, 1, 0, 0)])
+def test_a_key_beside_queries_of_no_heads_is_written(mods, monkeypatch, H, kv, T, calls):
+    _, ops, _ = mods
+    rec = _Lib(monkeypatch, ops, "qk_norm_rope")
+    q, k = torch.zeros(2, T, H, 64), torch.zeros(2, T, 64) if kv else None
+    ring = torch.zeros(2, 5, 64) if kv else None
+    ops.qk_norm_rope(q, k, torch.zeros_like(q), ring, torch.zeros(2, dtype=torch.int32), stream=rec.stream)
+    assert len(rec.calls) == calls
+    if calls:
+        a = rec.calls[0]
+        assert a[9] == H and (a[0] is None) == (H == 0) and a[3] == k.data_ptr() and a[21] == ring.data_ptr()
