@@ -396,6 +396,8 @@ def hca_paged_append(a, z, pos0, carry, pool, table, held, m, carry_out=None, le
     into carry_out.  Entries are optionally normalised and rotated at m * index."""
     dev, dt = _home(a), a.dtype
     B, T, D = a.shape
+    if not B:
+        return                       # (its tensors have no addresses)
     N, P_, _ = pool.shape
     maxp = table.shape[1]
     state = (B, 2, 3, D)

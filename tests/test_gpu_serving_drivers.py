@@ -267,3 +267,22 @@ def test_a_key_beside_queries_of_no_heads(mods, dt):
     ops.qk_norm_rope(None, k, None, rings[1], p, inv_freq=f)
     assert torch.equal(*rings) and not (rings[0] == 7.0).any()
     ops.qk_norm_rope(q, None, torch.empty_like(q), None, p, inv_freq=f)
+
+
+def test_calls_on_an_empty_batch(mods):
+    """No sequences, and no tokens: the calls return and write nothing (the carry of no
+    tokens is the carry)."""
+    _, ops, paged = mods
+    pool = torch.full((4, 2, 128), 9.0, device="cuda")
+    for B, T in ((0, 3), (2, 0)):
+        a, i = torch.zeros(B, T, 128, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+        tab = torch.zeros(B, 2, dtype=torch.int32, device="cuda")
+        carry = torch.randn(B, 2, 3, 128, device="cuda")
+        out = torch.zeros_like(carry)
+        ops.hca_paged_append(a, a, i, carry, pool, tab, i, 4, carry_out=out)
+        assert torch.equal(out, carry)
+        q = torch.zeros(B, T, 4, 128, device="cuda")
+        ops.qk_norm_rope(q, a, torch.empty_like(q), torch.empty_like(a), i)
+        ops.hca_prefix_attn_fwd(q, pool, tab, i, paged.PrefixGroups.singles(B), None, None, 1.0, 0, i, torch.empty_like(q), 4)
+    torch.cuda.synchronize()
+    assert (pool == 9.0).all()

@@ -162,3 +162,15 @@ def test_a_key_beside_queries_of_no_heads_is_written(mods, monkeypatch, H, kv, T
     if calls:
         a = rec.calls[0]
         assert a[9] == H and (a[0] is None) == (H == 0) and a[3] == k.data_ptr() and a[21] == ring.data_ptr()
+
+
+@pytest.mark.parametrize("B,T,calls", [(0, 3, 0), (0, 0, 0), (2, 0, 1), (2, 3, 1)])
+def test_append_of_an_empty_batch_is_no_call(mods, monkeypatch, B, T, calls):
+    """No sequences: nothing to do (the library refuses null pointers); no tokens: the
+    carry still goes on."""
+    _, ops, _ = mods
+    rec = _Lib(monkeypatch, ops, "hca_paged_append")
+    a, i = torch.zeros(B, T, 64), torch.zeros(B, dtype=torch.int32)
+    ops.hca_paged_append(a, a, i, torch.zeros(B, 2, 3, 64), torch.zeros(4, 2, 64), torch.zeros(B, 2, dtype=torch.int32), i, 4,
+                         stream=rec.stream)
+    assert len(rec.calls) == calls
