@@ -416,7 +416,8 @@ class HcaDecode:
 
     def load(self, x, lens=None):
         """Take prompts a, z, kv_raw [R, T, D] (row r's first lens[r] tokens; lens
-        int32 [R] on the device, T for all by default) behind what the rows hold."""
+        int32 [R] on the device, T for all by default) behind what the rows hold
+        (``free`` or ``reset`` those that are to start anew)."""
         R, T, _ = x["a"].shape
         nr = self.norm_rope or NormRope(norm=False)
         if self.cfg.W:
@@ -459,6 +460,20 @@ class HcaDecode:
     def entries(self):
         """Complete entries of every row, int32 [R] (what a fork shares)."""
         return torch.div(self.pos, self.cfg.m, rounding_mode="floor").to(torch.int32)
+
+    def reset(self, rows):
+        """Rows (list or int32 tensor) start again at position 0: what ``load`` brings
+        next is a new sequence.  (Rows out of range are ignored.)"""
+        rows = self.cache._list(rows)
+        every = torch.arange(self.cache.R, dtype=torch.int32, device=self.pos.device)
+        self.pos.masked_fill_((rows.view(-1, 1) == every).any(0), 0)
+
+    def free(self, rows):
+        """Rows give up their pages and start again.  (A cache of several layers is
+        freed once, the other layers ``reset``.)"""
+        rows = self.cache._list(rows)
+        self.cache.free(rows)
+        self.reset(rows)
 
     def copy_state(self, src, dst, done=None):
         """Rows dst take the window, carry and position of rows src (int64 index

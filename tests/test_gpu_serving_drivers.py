@@ -286,3 +286,29 @@ def test_calls_on_an_empty_batch(mods):
         ops.hca_prefix_attn_fwd(q, pool, tab, i, paged.PrefixGroups.singles(B), None, None, 1.0, 0, i, torch.empty_like(q), 4)
     torch.cuda.synchronize()
     assert (pool == 9.0).all()
+
+
+@pytest.mark.parametrize("nr", [False, True])
+def test_a_freed_row_takes_a_new_prompt(mods, nr):
+    """A row that was freed in the middle of a block gives, with its next prompt, the bits
+    of a row that was never used; in a second layer too."""
+    layer, _, paged = mods
+    kw = dict(R=2, L=2, m=8, norm_rope=rope(layer) if nr else None)
+    c, d = decode(mods, **kw)
+    _, e = decode(mods, cache=c, layer_at=1, **kw)
+    c2, f = decode(mods, **kw)
+    x = {k: v for k, v in tokens(2, 45).items() if k != "q"}
+    y = tokens(2, 30, seed=9)
+    c.reserve([0, 1], [8, 8])
+    d.load(x), e.load(x)
+    d.free([1]), e.reset([1])
+    c.reserve([1], [8]), c2.reserve([0, 1], [8, 8])
+    only = torch.tensor([0, 29], dtype=torch.int32).cuda()
+    new = {k: v[:, :29].contiguous() for k, v in y.items() if k != "q"}
+    d.load(new, only), e.load(new, only), f.load(new, only)
+    for lay in (d, e, f):
+        lay.groups = paged.PrefixGroups([([1], 0)], 2)
+    outs = [lay.step(one(y, 29))[1].clone() for lay in (d, e, f)]
+    torch.cuda.synchronize()
+    assert c.status.item() == 0 and d.pos.tolist() == e.pos.tolist() == [45, 30]
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])

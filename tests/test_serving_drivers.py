@@ -174,3 +174,19 @@ def test_append_of_an_empty_batch_is_no_call(mods, monkeypatch, B, T, calls):
     ops.hca_paged_append(a, a, i, torch.zeros(B, 2, 3, 64), torch.zeros(4, 2, 64), torch.zeros(B, 2, dtype=torch.int32), i, 4,
                          stream=rec.stream)
     assert len(rec.calls) == calls
+
+
+def test_freed_rows_start_again(mods, monkeypatch):
+    _, ops, _ = mods
+    d = decode(mods)
+    freed = []
+    monkeypatch.setattr(ops, "kv_pages_free", lambda rows, *a: freed.append(rows.tolist()))
+    before = d.pos.clone()
+    d.free([2, 9, 0, 2])                      # (a cache takes lists of up to R rows)
+    assert freed == [[2, 9, 0, 2]]
+    before[[0, 2]] = 0
+    assert torch.equal(d.pos, before)
+    d.reset(torch.tensor([1, -1], dtype=torch.int32))
+    assert d.pos.tolist()[1] == 0 and freed == [[2, 9, 0, 2]]
+    d.free([])
+    assert d.pos[3] == before[3]
