@@ -404,7 +404,7 @@ class HcaDecode:
         self.groups = groups or paged.PrefixGroups.singles(R, device=device)
         # the window's, append, attention, positions (with a norm_rope the first is the queries' too)
         self.launches = 4 + norm_rope.launches - 2 if norm_rope is not None else 4 if cfg.W else 3
-        self.graph = self.captured = None
+        self.graph = None
 
     def _append(self, a, z, lens=None):
         nr = self.norm_rope
@@ -515,7 +515,8 @@ class HcaDecode:
                 self.step(x)
         torch.cuda.current_stream().wait_stream(s)
         self.graph = g
-        self.captured = (x, self.groups)       # (the graph reads them for as long as it lives)
+        # for as long as the graph lives, also behind a later capture with others
+        g.reads = (x, self.groups, self.norm_rope, self.sink)
         return g
 
     def replay(self):

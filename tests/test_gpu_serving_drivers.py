@@ -312,3 +312,27 @@ def test_a_freed_row_takes_a_new_prompt(mods, nr):
     torch.cuda.synchronize()
     assert c.status.item() == 0 and d.pos.tolist() == e.pos.tolist() == [45, 30]
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
+
+
+def test_two_captures_replayed_in_turn(mods):
+    """The graph of an earlier capture goes on with its own groups and inputs, although
+    nothing else holds them and their memory would be in use again."""
+    layer, _, paged = mods
+    c, d = decode(mods, R=4)
+    c.reserve([0, 1, 2, 3], [16] * 4)
+    d.load({k: v for k, v in tokens(4, 30).items() if k != "q"})
+    d.step(one(tokens(4, 1, seed=1)))
+    graphs = []
+    for b in (2, 1):
+        d.groups = paged.PrefixGroups([([b], 0)], 4)
+        graphs.append(d.capture(one(tokens(4, 1, seed=2))))
+    d.groups = paged.PrefixGroups.singles(4)
+    keep = [torch.full((k,), -1, dtype=torch.int32, device="cuda") for k in (1, 2, 4) for _ in range(32)]
+    for g, b in ((graphs[0], 2), (graphs[1], 1), (graphs[0], 2)):
+        pos, out = d.pos.clone(), d.out.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        pos[b] += 1
+        assert torch.equal(d.pos, pos)
+        assert [not torch.equal(d.out[r], out[r]) for r in range(4)] == [r == b for r in range(4)]
+    assert c.status.item() == 0 and len(keep) == 96

@@ -190,3 +190,39 @@ def test_freed_rows_start_again(mods, monkeypatch):
     assert d.pos.tolist()[1] == 0 and freed == [[2, 9, 0, 2]]
     d.free([])
     assert d.pos[3] == before[3]
+
+
+def test_every_capture_holds_what_its_graph_reads(mods, monkeypatch):
+    """Groups and inputs are the caller's to replace: a second capture must not release
+    those of the first, whose graph may still be replayed."""
+    import gc
+    import weakref
+    _, ops, paged = mods
+
+    class Stream:
+        def wait_stream(self, s):
+            pass
+
+    class Graph:
+        pass
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", Graph)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "graph", lambda g, stream: contextlib.nullcontext())
+    for name in ("qk_norm_rope", "hca_paged_append", "hca_prefix_attn_fwd", "csa_pos_advance"):
+        monkeypatch.setattr(ops, name, lambda *a, **k: None)
+    d = decode(mods)
+    graphs, refs = [], []
+    for b in range(2):
+        d.groups = paged.PrefixGroups([([b], 0)], 4, device="cpu")
+        x = {k: torch.zeros(4, 64) for k in ("a", "z", "kv_raw")} | {"q": torch.zeros(4, 2, 64)}
+        graphs.append(d.capture(x))
+        refs += [weakref.ref(d.groups), weakref.ref(x["q"])]
+        del x
+    d.groups = paged.PrefixGroups.singles(4, device="cpu")
+    gc.collect()
+    assert all(r() is not None for r in refs) and d.graph is graphs[1]
+    del graphs[0]
+    gc.collect()
+    assert refs[0]() is None and refs[2]() is not None
