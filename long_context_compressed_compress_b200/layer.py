@@ -83,8 +83,14 @@ class NormRope:
         ops.qk_norm_rope(q, kv, q_out, kv_out, q_pos0, q_weight=self.q_weight, kv_weight=self.kv_weight, lens=lens,
                          **self._kw())
 
+    def append(self, a, z, pos0, carry, pool, table, held, m, **kw):
+        """HCA entries, normalised and rotated as they are pooled."""
+        ops.hca_paged_append(a, z, pos0, carry, pool, table, held, m, weight=self.entry_weight, **self._kw(), **kw)
+
     def entries(self, kv_c, m, zeros):
-        """Entries [B, S, D] of a prefill, in place."""
+        """CSA entries [B, S, D] of a prefill, in place: those of the layer without the
+        norm, already of its type (half a step of it that fp32 entries, twice the bytes
+        and a pass more, would save)."""
         if kv_c.numel():
             ops.qk_norm_rope(None, kv_c, None, kv_c, zeros, kv_weight=self.entry_weight, pos_step=m, **self._kw())
 
@@ -204,17 +210,24 @@ class HcaPrefill:
         if norm_rope is not None:
             self.q_n = torch.empty_like(self.out)
             self.raw_n = torch.empty((c.B, c.T, c.D), dtype=dt, device=device)
-            self.launches += norm_rope.launches
+            # kv_c as a page a sequence, for the append that a decode uses
+            self.page = torch.arange(c.B, dtype=torch.int32, device=device).view(c.B, 1)
+            self.held = torch.ones((c.B,), dtype=torch.int32, device=device)
+            self.carry = torch.empty((c.B, 2, 3, c.D), dtype=torch.float32, device=device)
+            self.launches += norm_rope.launches - 1
 
     def run(self, x, timer=None):
         c = self.cfg
         t = timer or _no_timer
-        with t("hca_compress"):
-            ops.hca_compress(x["a"], x["z"], c.m, self.kv_c)
         q, raw = x["q"], x["kv_raw"]
-        if self.norm_rope is not None:
+        if self.norm_rope is None:
+            with t("hca_compress"):
+                ops.hca_compress(x["a"], x["z"], c.m, self.kv_c)
+        else:
+            # an entry is normalised from its 32-bit sums, to the bits that HcaDecode gives it
+            with t("hca_paged_append"):
+                self.norm_rope.append(x["a"], x["z"], self.q_pos0, self.carry, self.kv_c, self.page, self.held, c.m)
             with t("qk_norm_rope"):
-                self.norm_rope.entries(self.kv_c, c.m, self.q_pos0)
                 self.norm_rope.queries(q, raw, self.q_n, self.raw_n, self.q_pos0)
             q, raw = self.q_n, self.raw_n
         with t("hca_dense_attn_fwd"):
@@ -407,12 +420,9 @@ class HcaDecode:
         self.graph = None
 
     def _append(self, a, z, lens=None):
-        nr = self.norm_rope
         c = self.cache
-        kw = {} if nr is None else dict(norm=nr.norm, weight=nr.entry_weight, eps=nr.eps, inv_freq=nr.inv_freq,
-                                        interleaved=nr.interleaved)
-        ops.hca_paged_append(a, z, self.pos, self.carry, c.pool[self.layer], c.table, c.held, self.cfg.m, lens=lens,
-                             status=c.status, **kw)
+        append = ops.hca_paged_append if self.norm_rope is None else self.norm_rope.append
+        append(a, z, self.pos, self.carry, c.pool[self.layer], c.table, c.held, self.cfg.m, lens=lens, status=c.status)
 
     def load(self, x, lens=None):
         """Take prompts a, z, kv_raw [R, T, D] (row r's first lens[r] tokens; lens

@@ -336,3 +336,40 @@ def test_two_captures_replayed_in_turn(mods):
         assert torch.equal(d.pos, pos)
         assert [not torch.equal(d.out[r], out[r]) for r in range(4)] == [r == b for r in range(4)]
     assert c.status.item() == 0 and len(keep) == 96
+
+
+@pytest.mark.parametrize("dt,D,m,T", [("bf16", 128, 64, 700), ("bf16", 128, 128, 129), ("bf16", 128, 4, 333),
+                                      ("f32", 64, 16, 90)])
+def test_entries_of_a_prefill_are_those_of_a_decode(mods, dt, D, m, T):
+    """A prompt's normalised, rotated entries: the same bits through HcaPrefill and
+    HcaDecode.load, one rounding from the formula.  The pooled sums' error, relative
+    to mean |a| (below 2 for these inputs): 2 (2 m + 64) half steps of fp32, over the
+    row's rms; the norm and rotation 40 more, both times |w| of a pair; then half a step
+    of the type."""
+    layer, ops, paged = mods
+    from long_context_compressed_compress_b200 import configs
+    B, H = 2, 16
+    cfg = configs._hca(B=B, T=T, H=H, D=D, m=m, W=20, dtype=dt, tau=0.1)
+    t = torch.bfloat16 if dt == "bf16" else torch.float32
+    x = tokens(B, T, D=D, H=H, dt=t, seed=4) | {"sink": None}
+    nr = rope(layer, D)
+    nr.entry_weight = torch.linspace(1.5, 0.5, D).cuda()
+    p = layer.HcaPrefill(cfg, norm_rope=nr)
+    p.kv_c.fill_(9.0)
+    p.run(x)
+    cache = paged.PagedEntries(1, 2 * B * (T // m + 1), 1, D, B, T // m + 1, dtype=t)
+    d = layer.HcaDecode(cfg, cache, norm_rope=nr)
+    cache.reserve(list(range(B)), [T // m] * B)
+    d.load({k: x[k] for k in ("a", "z", "kv_raw")})
+    torch.cuda.synchronize()
+    assert cache.status.item() == 0 and ops.device_status() == 0
+    S = T // m
+    got = cache.pool[0][cache.table[:, :S].long()].reshape(B, S, D)
+    assert torch.equal(got, p.kv_c[:, :S])
+    w = np64(nr.entry_weight)
+    for b in range(B):
+        ent, _ = serving.append(np64(x["z"][b]), np64(x["a"][b]), T, m)
+        ref = serving.norm_rope(ent, m * np.arange(S), np64(nr.inv_freq), w)
+        rms = np.sqrt((ent ** 2).mean(-1, keepdims=True))
+        tol = (2 * (2 * m + 64) * 2 / rms + 40) * 2.0 ** -24 * 2 * w.max() * 3 + torch.finfo(t).eps / 2 * np.abs(ref) * 1.001
+        assert (np.abs(np64(got[b]) - ref) <= tol).all()
