@@ -429,6 +429,8 @@ class HcaDecode:
         int32 [R] on the device, T for all by default) behind what the rows hold
         (``free`` or ``reset`` those that are to start anew)."""
         R, T, _ = x["a"].shape
+        if x["z"].shape != x["a"].shape or x["kv_raw"].shape != x["a"].shape:
+            raise ValueError("a, z and kv_raw must be of one shape [R, T, D]")
         nr = self.norm_rope or NormRope(norm=False)
         if self.cfg.W:
             nr.queries(None, x["kv_raw"], None, self.ring, self.pos, lens)

@@ -226,3 +226,19 @@ def test_every_capture_holds_what_its_graph_reads(mods, monkeypatch):
     del graphs[0]
     gc.collect()
     assert refs[0]() is None and refs[2]() is not None
+
+
+@pytest.mark.parametrize("name", ["z", "kv_raw"])
+def test_a_prompt_of_uneven_lengths_is_refused_untouched(mods, monkeypatch, name):
+    """Positions advance by a's tokens: a window of more or fewer would be off."""
+    _, ops, _ = mods
+    calls = []
+    for n in ("qk_norm_rope", "hca_paged_append"):
+        monkeypatch.setattr(ops, n, lambda *a, **k: calls.append(a))
+    d = decode(mods)
+    before = d.pos.clone()
+    x = {k: torch.zeros(4, 5, 64) for k in ("a", "z", "kv_raw")}
+    x[name] = torch.zeros(4, 6, 64)
+    with pytest.raises(ValueError):
+        d.load(x)
+    assert not calls and torch.equal(d.pos, before)
