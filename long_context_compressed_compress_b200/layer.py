@@ -443,6 +443,8 @@ class HcaDecode:
         c = self.cfg
         t = timer or _no_timer
         R = self.cache.R
+        if self.groups.B != R:                # (before anything of the step is done)
+            raise ValueError(f"groups of a batch of {self.groups.B} for a cache of {R} rows")
         live = self.groups.attended           # (as lengths: one token, or none; None: all rows)
         q, raw = x["q"].view(R, 1, c.H, c.D), x["kv_raw"].view(R, 1, c.D)
         if self.norm_rope is not None:

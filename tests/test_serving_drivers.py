@@ -242,3 +242,22 @@ def test_a_prompt_of_uneven_lengths_is_refused_untouched(mods, monkeypatch, name
     with pytest.raises(ValueError):
         d.load(x)
     assert not calls and torch.equal(d.pos, before)
+
+
+@pytest.mark.parametrize("B", [3, 5])
+def test_groups_of_another_batch_are_refused_untouched(mods, monkeypatch, B):
+    """Nothing of the step is done: a token pooled without its position would be pooled
+    again by the next."""
+    _, ops, paged = mods
+    calls = []
+
+    def attn(q, *a, **k):
+        raise ValueError("groups must be those of the batch, on its device")
+    monkeypatch.setattr(ops, "hca_prefix_attn_fwd", attn)
+    for n in ("qk_norm_rope", "hca_paged_append", "csa_ring_append", "csa_pos_advance"):
+        monkeypatch.setattr(ops, n, lambda *a, **k: calls.append(a))
+    d = decode(mods)
+    d.groups = paged.PrefixGroups.singles(B, device="cpu")
+    with pytest.raises(ValueError):
+        d.step({k: torch.zeros(4, 64) for k in ("a", "z", "kv_raw")} | {"q": torch.zeros(4, 2, 64)})
+    assert not calls
