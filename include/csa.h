@@ -462,7 +462,9 @@ int hca_paged_append(const void* a, const void* z, int dtype, int B, int T,
  * hca_prefix_attn_fwd -- HCA attention ([cf-1] §3.2, §3.3) of a batch over paged
  * entries, for groups of sequences whose leading entries are the same pages.
  * Same result as hca_dense_attn_fwd over each sequence's own entries (window
- * and sink fused); what a group shares is read once for its sequences.
+ * and sink fused).  On tcgen05 a group's shared entries are loaded once for up to
+ * 128 of its query rows (128 / H sequences), which meet in L2; on CUDA cores each
+ * sequence loads its own.
  *   q, out [B, T, H, D]: query row t of sequence b is at position q_pos0[b] + t
  *   pool [N, P, D], table [B, max_pages], held [B]: visible entries
  *     s < (p + 1) / m whose page is not held (or out of range) are skipped
@@ -476,7 +478,10 @@ int hca_paged_append(const void* a, const void* z, int dtype, int B, int T,
  * Deterministic: a row's result depends on the row, its keys, H, W and
  * max_pages * P, not on the batch, the grouping or T.
  * bf16 with D = 128 and H <= 128 runs on tcgen05, the rest on CUDA cores
- * (H <= 1024).  Requires D in {64, 128}, P >= 1, 16-byte aligned tensors.
+ * (H <= 1024).  On tcgen05 the weights are rounded to bf16 for their product with
+ * the keys, and the output is divided by the sum of the rounded ones (lse is that
+ * of the weights in fp32); a row in which a weight passes 2^100 times the largest
+ * of its first tile is done again in fp32 at some 0.5 us a key.  Requires D in {64, 128}, P >= 1, 16-byte aligned tensors.
  * status: optional device status word.
  */
 int hca_prefix_attn_fwd(const void* q, const void* pool, int N, int P,

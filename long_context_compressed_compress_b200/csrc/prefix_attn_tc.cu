@@ -6,7 +6,7 @@
 // A job is up to 128 query rows, whole (sequence, token) pairs of H heads of one
 // group, as the M side of the MMAs; thread = row in the softmax:
 //   S [128 rows x 128 keys] = Q K^T   (Q and the key tile in shared memory)
-//   O [128 rows x 128 dims] += P K    (P in tensor memory over S; the same tile
+//   O [128 rows x 128 dims] += P K    (P in tensor memory beside S; the same tile
 //                                      read with its dims as N)
 // Key tiles come in three kinds:
 //   shared  128 entries that every row of the job sees, loaded once for all;
@@ -33,7 +33,10 @@
 // precision at any scale, so M only has to keep them in range.  A row in which
 // a later weight passes 2^100 is flagged and computed again, exactly, on CUDA
 // cores with a running maximum; a weight below 2^-126 of the first tile's
-// largest is lost against it anyway.  So once M is there a tile needs no maximum and no
+// largest is lost against it anyway.  (Such a row costs 0.5 us a key, a warp's rows
+// one after the other: with one of 16 rows over 1024 entries 0.56 ms for 15 us, over
+// 8192 4.1 ms for 20 us, all 16 of them 8.6 ms.  Logits that differ by 69 within a
+// row; with normalised q and k they are bounded by tau D times the norms' weights.)  So once M is there a tile needs no maximum and no
 // word from the tiles before (a running one took a third of a tile's time).
 // P is rounded to bf16 for the MMA (a half step of 2^-8 a weight, of the size
 // of the output's own rounding).  A row has two sums of its weights, by tile parity
@@ -1208,7 +1211,12 @@ int launch_prefix_attn_tc(const PrefixAttnArgs& base, cudaStream_t st) {
   // Few heads make few jobs, so up to eight ranks; many heads make a job
   // a sequence, and four.  (32 of 16 heads, 66 tiles: 28.3 us with 4 ranks, 21.6 with 8; 32
   // of 64 heads, 18 tiles: 18.2 us with 4, 31.5 with 8, whose clusters do not all run at
-  // once; 4 of 64 heads, 34 tiles: 20.0 and 17.0.)
+  // once; 4 of 64 heads, 34 tiles: 20.0 and 17.0.)  From 128 tiles on a sequence that
+  // fills them is what takes long, and many heads have eight ranks too: 1, 4 and 12
+  // sequences of 128 heads over 16384 entries 26.9, 27.4 and 28.8 us (with four 40.1,
+  // 40.8, 41.2), over 32768 40.5, 41.3, 45.4 (67.7, 68.3, 73.0).  Batches whose clusters
+  // do not all run at once pay for it: 32 of them 85.5 us for 47.6, and 41.8 for 16.6
+  // if each has but 1000 entries in use.
   const long long tiles = (static_cast<long long>(a.max_pages) * a.P + kTile - 1) / kTile;
   const int most_c = a.H > 32 && tiles < 128 ? 4 : 8;
   a.c = 1;

@@ -65,7 +65,10 @@ class NormRope:
     ones) and their last 2 * len(inv_freq) dims rotated by position * inv_freq
     (float64, radians per token); an entry is at its block's first position, m * s.
     Since keys are values too, ``derotate`` turns the attention's output back by
-    the query's position, so that it depends on relative positions only."""
+    the query's position, so that it depends on relative positions only.
+
+    ``CsaPrefill``, ``HcaPrefill`` and ``HcaDecode`` take one; ``CsaDecode``, its
+    snapshots and ``Stack`` do not, so a CSA layer with it is for prefills alone."""
 
     inv_freq: Optional[torch.Tensor] = None
     q_weight: Optional[torch.Tensor] = None
