@@ -515,6 +515,8 @@ class HcaDecode:
         cache of several layers is forked once, the other layers' states copied by
         their own ``copy_state(src, dst, cache.forked())``."""
         src, dst = self.cache._list(src), self.cache._list(dst)
+        if src.shape != dst.shape:
+            raise ValueError(f"{src.numel()} rows to fork into {dst.numel()}")
         if not dst.numel():
             return
         self.cache.fork(src, dst, self.entries()[self._in_range(src)])

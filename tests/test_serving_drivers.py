@@ -261,3 +261,14 @@ def test_groups_of_another_batch_are_refused_untouched(mods, monkeypatch, B):
     with pytest.raises(ValueError):
         d.step({k: torch.zeros(4, 64) for k in ("a", "z", "kv_raw")} | {"q": torch.zeros(4, 2, 64)})
     assert not calls
+
+
+@pytest.mark.parametrize("src,dst", [([0], []), ([], [1]), ([0, 1], [2])])
+def test_fork_of_lists_of_unlike_lengths_is_refused(mods, monkeypatch, src, dst):
+    _, ops, _ = mods
+    monkeypatch.setattr(ops, "kv_pages_fork", lambda *a: pytest.fail("called"))
+    d = decode(mods)
+    before = d.pos.clone()
+    with pytest.raises(ValueError):
+        d.fork(src, dst)
+    assert torch.equal(d.pos, before)
